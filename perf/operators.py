@@ -14,7 +14,7 @@ import torch
 
 own = False
 
-PAGE_EXP_MIN, PAGE_EXP_MAX = -64, 120  # range of a page's shared exponent
+PAGE_EXP_MIN, PAGE_EXP_MAX = -40, 40  # range of a page's shared exponent
 E4M3_MAX = 448.0
 DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 
