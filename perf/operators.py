@@ -211,8 +211,10 @@ def _run_own(s):
         return fq.int8_matmul(s["a"], s["a_scale"], s["w"], s["w_scale"], out_dtype=DTYPES[case["out"]])
     if op == "linear":
         if "plan" not in s:
-            s["plan"] = fq.FlatQuant(case["tokens"], case["M"], case["N"], s["x"].dtype)
-        codes, qs = s["plan"].quantize_per_token(s["x"], s["P1"], s["P2"], clip_ratio=case["clip"], out_dtype="int8")
+            s["plan"] = (fq.FlatQuant(case["tokens"], case["M"], case["N"], s["x"].dtype),
+                         s["P1"].contiguous(), s["P2"].contiguous())
+        plan, P1, P2 = s["plan"]
+        codes, qs = plan.quantize_per_token(s["x"], P1, P2, clip_ratio=case["clip"], out_dtype="int8")
         return fq.int8_matmul(codes, qs, s["w"], s["w_scale"], out_dtype=s["x"].dtype), qs
     if "plan" not in s:
         s["plan"] = fq.KVCache.from_buffers(s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"])
