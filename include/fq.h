@@ -12,7 +12,8 @@
  *
  *   per-token ("per-token mode"): quantScale[k] = max|x''| / (7 / clipRatio) (float32),
  *       out = round_half_even(x'' / quantScale) clamped to [-8, 7], as INT4 (two per
- *       byte) or INT4 packed eight per INT32 word (the same bytes);
+ *       byte) or INT4 packed eight per INT32 word (the same bytes); or the same rule with
+ *       INT8 codes: quantScale[k] = max|x''| / (127 / clipRatio), codes in [-128, 127];
  *   per-group ("per-group mode", cases 1-3): x'' viewed as [K, M*N] in groups of 32;
  *       one E8M0 exponent per group in a [K, ceilDiv(M*N, 64), 2] byte tensor, and one
  *       E2M1 code per element, two per byte, out [K, M*N / 2] bytes.
@@ -65,8 +66,11 @@ typedef enum {
     FQ_ERR_DEVICE_TIMEOUT = 161005 /* a bounded wait inside a kernel gave up (see fq_device_status) */
 } fq_status;
 
-typedef enum { FQ_BF16 = 0, FQ_FP16 = 1 } fq_dtype;          /* x, P1, P2 share one type */
-typedef enum { FQ_OUT_INT4 = 0, FQ_OUT_INT32 = 1 } fq_int_out;
+typedef enum {
+    FQ_BF16 = 0, FQ_FP16 = 1,   /* x, P1, P2 share one type */
+    FQ_FP32 = 2                 /* an output type of fq_int8_matmul only */
+} fq_dtype;
+typedef enum { FQ_OUT_INT4 = 0, FQ_OUT_INT32 = 1, FQ_OUT_INT8 = 2 } fq_int_out;
 
 /* Kernel selection, for tests and benchmarks. AUTO picks the tensor-core kernel where
  * the shape allows it and the general kernel elsewhere. */
@@ -94,7 +98,11 @@ FQ_API fq_status fq_destroy(fq_handle *h);
  *   P2         [N, N]     right matrix (kroneckerP2); must not be NULL in this mode
  *   clipRatio  in (0, 1]
  *   fmt        FQ_OUT_INT4: out is [K, M, N] INT4, K*M*N/2 bytes (N even);
- *              FQ_OUT_INT32: out is [K, M, N/8] int32 (N % 8 == 0), the same bytes
+ *              FQ_OUT_INT32: out is [K, M, N/8] int32 (N % 8 == 0), the same bytes;
+ *              FQ_OUT_INT8: out is [K, M, N] int8, K*M*N bytes (any N), one two's complement
+ *              code per byte, and 127 takes the place of 7 in quantScale. This format is an
+ *              addition of this library (the page stops at 4 bits): the activations of
+ *              fq_int8_matmul
  *   quantScale [K] float32
  * Errors: FQ_ERR_NULLPTR (h, x, P1, P2, out, quantScale), FQ_ERR_INVALID (clipRatio out
  * of range, N odd, N % 8 != 0 for INT32, unknown fmt, misaligned pointer), FQ_ERR_CUDA. */
@@ -147,6 +155,133 @@ FQ_API fq_status fq_mx_matmul(int64_t T, int64_t O, int64_t L, const void *a_fp4
                               const uint8_t *a_scale_e8m0, const void *w_fp4,
                               const uint8_t *w_scale_e8m0, float *C, uint32_t *status,
                               struct CUstream_st *stream);
+
+/* INT8 x INT8 product with a scale for each token and each output channel: the consumer of
+ * fq_quantize_per_token's FQ_OUT_INT8 codes (a, a_scale = quantScale) for weights quantized
+ * the same way, one scale per row:
+ *
+ *     C[t, o] = (sum_i a[t, i] * w[o, i]) * a_scale[t] * w_scale[o]
+ *
+ * The sum is exact (int32 on the tensor cores); it is rounded once to float32, multiplied by
+ * a_scale[t], then by w_scale[o] in float32 and rounded once to the output type.
+ *   T, O       rows of a and of w, in [1, 262144]
+ *   L          codes per row, a multiple of 16 in [16, 65536]
+ *   a, w       [T, L] and [O, L] int8, 16-byte aligned
+ *   out_type   FQ_BF16, FQ_FP16 or FQ_FP32: the type of C [T, O], row-major, aligned to its
+ *              elements
+ *   status     a device word, or NULL: as in fq_mx_matmul
+ * Allocates nothing; asynchronous on stream. Errors: FQ_ERR_NULLPTR (a, a_scale, w, w_scale,
+ * C), FQ_ERR_INVALID (a size or type out of range, L % 16 != 0, misaligned pointer),
+ * FQ_ERR_CUDA. */
+FQ_API fq_status fq_int8_matmul(int64_t T, int64_t O, int64_t L, const int8_t* a, const float* a_scale,
+                                const int8_t* w, const float* w_scale, fq_dtype out_type, void* C,
+                                uint32_t* status, struct CUstream_st* stream);
+
+/* Paged key / value cache held in 8 bits (an addition of this library, like everything that
+ * takes an fq_kv_cache). A page holds page_size consecutive tokens of one sequence. The
+ * values of one page and one head share one power of two, kept as an E8M0 byte like the
+ * scales of the per-group mode; each value is an E4M3 code:
+ *
+ *     value[page, head, row, d] = e4m3(code[page, head, row, d]) * 2^(scale[page, head] - 127)
+ *
+ * The byte of a page is e + 127, e the smallest exponent with max|value| <= 448 * 2^e over the
+ * page's tokens, clamped to [-40, 40] (an all-zero page gets -40; larger magnitudes saturate).
+ *   num_pages   in [1, 2^31 - 1], with num_pages * kv_heads * page_size * head_dim / 128 below
+ *               2^31 (codes may pass 4 GB)
+ *   kv_heads    in [1, 256];  page_size 16, 32, 64 or 128;  head_dim 64 or 128
+ *   k, v        [num_pages, kv_heads, page_size, head_dim] E4M3 codes, 16-byte aligned
+ *   k_scale, v_scale  [num_pages, kv_heads] E8M0 bytes (as fq_kv_append writes them, in
+ *               [87, 167]) */
+typedef struct {
+    void *k, *v;
+    uint8_t *k_scale, *v_scale;
+    int64_t num_pages;
+    int32_t kv_heads, page_size, head_dim;
+} fq_kv_cache;
+
+/* The sequences of one call, as device arrays (the library reads them on the device only, so a
+ * captured graph may be replayed with other contents):
+ *   cu_new      [num_seqs + 1] int32, rising from 0: the new tokens of sequence b are rows
+ *               cu_new[b] .. cu_new[b + 1] - 1 of the token arrays; a sequence may have none.
+ *               Rows behind cu_new[num_seqs] are left alone
+ *   seq_lens    [num_seqs] int32: tokens of sequence b with its new ones (its new tokens are
+ *               the last ones); may be 0
+ *   page_table  [num_seqs, table_width] int32: tokens j * page_size .. of sequence b lie in page
+ *               page_table[b, j]; entries past a sequence's last page are not read
+ * num_seqs in [1, 65536], table_width in [1, 2^24].
+ * Contents that are out of range are refused on the device, and FQ_KV_BAD_BATCH is set in the
+ * call's status word: a sequence with more new tokens than its length, or rows outside [0, T),
+ * or (attention) a length past max_seq_len gets neither pages nor outputs written; a token whose
+ * page lies outside the table or the cache is not stored, and not attended to. */
+typedef struct {
+    const int32_t *cu_new, *seq_lens, *page_table;
+    int32_t num_seqs, table_width;
+} fq_kv_batch;
+
+#define FQ_KV_BAD_BATCH 0x100u /* status bit: the batch's contents are out of range */
+
+/* Appends the new tokens' keys and values to the cache, rotating keys (and queries) on the way.
+ *   T           rows of the token arrays, in [1, 2^24]
+ *   dtype       FQ_BF16 or FQ_FP16, of k, v, q and q_out
+ *   k, v        [T, kv_heads, head_dim]; the heads of one token are contiguous, tokens are
+ *               k_stride / v_stride elements apart (slices of one fused projection may be passed)
+ *   inv_freq    [rot_dim / 2] float32, or NULL with rot_dim = 0 (no rotation). The pair j of the
+ *               token at position pos (0 for the first token of its sequence) is turned by the
+ *               angle pos * inv_freq[j]. The pair is (d, d + rot_dim / 2), d = j, or with
+ *               interleaved = 1 (2j, 2j + 1); elements from rot_dim on are kept. The angle is
+ *               formed and reduced in float64, the rotation in float32. rot_dim a multiple of 16,
+ *               at most head_dim
+ *   q, q_out    [T, q_heads, head_dim] (q tokens q_stride apart, q_out contiguous): the queries,
+ *               rotated alike and rounded once to dtype; both NULL with q_heads = 0
+ * A page that already holds tokens of the sequence keeps the larger of its exponent and the new
+ * tokens'; when it grows, the codes of the older tokens are rounded once more (exact but for
+ * codes that become subnormal). Rows that belong to no token are not written. The pages that
+ * receive tokens belong to one sequence each: two sequences appending to one page race.
+ *   status      a device word, or NULL
+ * Strides are multiples of 8 elements, pointers 16-byte aligned. Allocates nothing;
+ * asynchronous on stream; deterministic. Errors: FQ_ERR_NULLPTR, FQ_ERR_INVALID, FQ_ERR_CUDA. */
+FQ_API fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch, int64_t T, fq_dtype dtype,
+                              const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              const float *inv_freq, int32_t rot_dim, int interleaved,
+                              const void *q, int64_t q_stride, int32_t q_heads, void *q_out,
+                              uint32_t *status, struct CUstream_st *stream);
+
+/* Attention of the new tokens' queries over the cache: for query head h and key / value head
+ * h / (q_heads / kv_heads)
+ *
+ *     out[t, h] = sum_j softmax_j(scale * q[t, h] . key[j]) value[j]
+ *
+ * over the tokens j of t's own sequence: all of them, or with causal = 1 those up to t itself.
+ *   q           [T, q_heads, head_dim], tokens q_stride elements apart; T in [1, 2^24]
+ *   q_heads     a multiple of kv_heads, at most 1024
+ *   max_q_len   an upper bound of the sequences' new tokens (in [1, T]); queries past it are not
+ *               computed (FQ_KV_BAD_BATCH)
+ *   max_seq_len an upper bound of seq_lens, in [1, table_width * page_size]; a longer sequence is
+ *               not computed (FQ_KV_BAD_BATCH). The work is divided by it, so a close bound is
+ *               faster
+ *   scale       finite
+ *   out         [T, q_heads, head_dim] of dtype, contiguous. A query that sees no token gets 0
+ *   lse         [T, q_heads] float32, or NULL: log sum_j exp(scale * q . key[j]); -inf for a
+ *               query that sees no token
+ *   workspace   at least fq_kv_attention_workspace(...) bytes, 16-byte aligned (NULL when that is
+ *               0). It holds partial results during the call only; calls that may overlap (on
+ *               two streams, or two captured graphs) need one each
+ * Sums, maxima and the softmax are float32. Keys and values enter the products exactly (an E4M3
+ * code is an fp16 number); queries too, scaled by a power of two per row; the probabilities are
+ * rounded to fp16 for the second product. Stale rows of a page (behind the last token) are never
+ * used, whatever they hold. Allocates nothing; asynchronous on stream; deterministic. Errors:
+ * FQ_ERR_NULLPTR, FQ_ERR_INVALID (also a workspace that is too small), FQ_ERR_CUDA. */
+FQ_API fq_status fq_kv_attention(const fq_kv_cache *cache, const fq_kv_batch *batch, int64_t T, fq_dtype dtype,
+                                 const void *q, int64_t q_stride, int32_t q_heads, int32_t max_q_len,
+                                 int64_t max_seq_len, double scale, int causal, void *out, float *lse,
+                                 void *workspace, int64_t workspace_bytes, uint32_t *status,
+                                 struct CUstream_st *stream);
+
+/* Bytes of workspace that fq_kv_attention needs for these arguments on the current device, in
+ * *bytes (0 when the work is not split). Errors: FQ_ERR_NULLPTR, FQ_ERR_INVALID, FQ_ERR_CUDA. */
+FQ_API fq_status fq_kv_attention_workspace(const fq_kv_cache *cache, const fq_kv_batch *batch, int64_t T,
+                                           int32_t q_heads, int32_t max_q_len, int64_t max_seq_len,
+                                           int64_t *bytes);
 
 /* Per-group mode (as fq_quantize_mx) for callers that cannot allocate device memory.
  * The paper has no counterpart: this entry point is an addition of this library.

@@ -13,6 +13,9 @@ quantization fusion" (http://www.zwxr.cn/news/277566), sections "How it works",
 `consumer.py` restates the dequantization the page says the outputs are emitted for,
 and the FP4 x FP4 contraction that would consume them (no kernel for it exists yet).
 
+`serving.py` is the oracle of the 8-bit serving operators (INT8 codes and product, paged cache,
+attention over it), pinned by `tests/test_serving_host.py`.
+
 Parity unpinned: none. Every public function here is pinned against closed forms,
 brute force, hand-worked values or textbook special cases, by
 `tests/test_oracle_pins.py` (the operator) and `tests/test_oracle_consumer_pins.py`
@@ -44,3 +47,4 @@ from .consumer import (  # noqa: F401
     dequantize_mx,
     mx_matmul,
 )
+from . import serving  # noqa: F401

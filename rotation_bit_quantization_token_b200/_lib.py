@@ -15,14 +15,32 @@ FQ_ERR_CUDA = 161003
 FQ_ERR_UNSUPPORTED = 161004
 FQ_ERR_DEVICE_TIMEOUT = 161005
 
-FQ_BF16, FQ_FP16 = 0, 1
-FQ_OUT_INT4, FQ_OUT_INT32 = 0, 1
+FQ_BF16, FQ_FP16, FQ_FP32 = 0, 1, 2
+FQ_OUT_INT4, FQ_OUT_INT32, FQ_OUT_INT8 = 0, 1, 2
 FQ_KERNEL_AUTO, FQ_KERNEL_GENERAL, FQ_KERNEL_TCGEN05 = 0, 1, 2
+FQ_KV_BAD_BATCH = 0x100
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _dbl = ctypes.c_double
+
+_i32 = ctypes.c_int32
+
+
+class KvCacheDesc(ctypes.Structure):
+    """fq_kv_cache."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", _i64),
+                ("kv_heads", _i32), ("page_size", _i32), ("head_dim", _i32)]
+
+
+class KvBatchDesc(ctypes.Structure):
+    """fq_kv_batch."""
+    _fields_ = [("cu_new", _vp), ("seq_lens", _vp), ("page_table", _vp), ("num_seqs", _i32),
+                ("table_width", _i32)]
+
+
+_cache_p, _batch_p = ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc)
 
 _SIGNATURES = {
     "fq_create": (_int, [ctypes.POINTER(_vp), _i64, _i64, _i64, _int]),
@@ -32,6 +50,12 @@ _SIGNATURES = {
     "fq_debug_rotate": (_int, [_vp, _vp, _vp, _vp, _vp, _vp]),
     "fq_quantize_mx_static": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _dbl, _vp, _vp, _vp]),
     "fq_mx_matmul": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fq_int8_matmul": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp]),
+    "fq_kv_append": (_int, [_cache_p, _batch_p, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i32, _int,
+                            _vp, _i64, _i32, _vp, _vp, _vp]),
+    "fq_kv_attention": (_int, [_cache_p, _batch_p, _i64, _int, _vp, _i64, _i32, _i32, _i64, _dbl, _int,
+                               _vp, _vp, _vp, _i64, _vp, _vp]),
+    "fq_kv_attention_workspace": (_int, [_cache_p, _batch_p, _i64, _i32, _i32, _i64, ctypes.POINTER(_i64)]),
     "fq_static_device_status": (_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "fq_static_debug_arm_stall": (_int, [_dbl]),
     "fq_set_kernel": (_int, [_vp, _int]),

@@ -12,6 +12,7 @@ import torch
 from . import _lib
 
 _DT = {torch.bfloat16: _lib.FQ_BF16, torch.float16: _lib.FQ_FP16}
+_OUT_DT = {**_DT, torch.float32: _lib.FQ_FP32}
 
 
 def _stream_ptr(stream=None):
@@ -147,22 +148,25 @@ class FlatQuant:
 
     def quantize_per_token(self, x, P1, P2, clip_ratio=1.0, out_dtype="int4",
                            out=None, quant_scale=None, stream=None):
-        """Per-token INT4 quantization of P1 . (x . P2). Returns (out, quantScale):
-        out is uint8 [K, M*N/2] for "int4" or int32 [K, M, N/8] for "int32"."""
+        """Per-token INT4 or INT8 quantization of P1 . (x . P2). Returns (out, quantScale):
+        out is uint8 [K, M*N/2] for "int4", int32 [K, M, N/8] for "int32" or int8 [K, M*N]
+        for "int8" (the activations of int8_matmul)."""
         self._inputs(x, P1, P2)
         K, M, N = self.K, self.M, self.N
         if out is None:
-            if out_dtype == "int32":
+            if out_dtype == "int8":
+                out = torch.empty((K, M * N), dtype=torch.int8, device=x.device)
+            elif out_dtype == "int32":
                 out = torch.empty((K, M, N // 8), dtype=torch.int32, device=x.device)
             else:
                 out = torch.empty((K, M * N // 2), dtype=torch.uint8, device=x.device)
         else:
-            _check_output("out", out, K * M * N // 2, x.device)
+            _check_output("out", out, K * M * N // (1 if out_dtype == "int8" else 2), x.device)
         if quant_scale is None:
             quant_scale = torch.empty((K,), dtype=torch.float32, device=x.device)
         else:
             _check_output("quant_scale", quant_scale, 4 * K, x.device, torch.float32)
-        fmt = _lib.FQ_OUT_INT32 if out_dtype == "int32" else _lib.FQ_OUT_INT4
+        fmt = {"int32": _lib.FQ_OUT_INT32, "int8": _lib.FQ_OUT_INT8}.get(out_dtype, _lib.FQ_OUT_INT4)
         _lib.check(self._lib.fq_quantize_per_token(
             self._h, _ptr(x), _ptr(P1), _ptr(P2), float(clip_ratio), fmt, _ptr(out),
             _ptr(quant_scale), _stream_ptr(stream)), "fq_quantize_per_token")
@@ -243,6 +247,196 @@ def quantize_mx_static(x, P1, P2, dst_type_max=0.0, out=None, scales=None, strea
     return out, scales
 
 
+def int8_matmul(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, status=None, stream=None):
+    """C [T, O] = (a . w^T) * a_scale[:, None] * w_scale[None, :] for int8 a [T, L] and w [O, L]
+    with float32 scales (see fq_int8_matmul): a and a_scale as quantize_per_token gives them
+    with out_dtype="int8", w and w_scale alike for the weights' rows. out_dtype bfloat16,
+    float16 or float32. status: an int32 tensor of one element, ORed with a nonzero code if a
+    bounded wait inside the kernel gives up (the output is then undefined)."""
+    lib = _lib.load()
+    for name, t, dt, dims in (("a", a, torch.int8, 2), ("a_scale", a_scale, torch.float32, 1),
+                              ("w", w, torch.int8, 2), ("w_scale", w_scale, torch.float32, 1)):
+        _check_input(name, t, dt)
+        if t.dim() != dims:
+            raise ValueError(f"{name} must have {dims} dimension{'s' if dims > 1 else ''}")
+    if out_dtype not in _OUT_DT:
+        raise ValueError("out_dtype must be torch.bfloat16, torch.float16 or torch.float32")
+    T, L = a.shape
+    O = w.shape[0]
+    if w.shape[1] != L:
+        raise ValueError(f"w must have rows of {L} codes, got {w.shape[1]}")
+    if a_scale.numel() != T or w_scale.numel() != O:
+        raise ValueError("a_scale and w_scale must have one scale per row of a and of w")
+    _check_device(a, a_scale=a_scale, w=w, w_scale=w_scale)
+    if out is None:
+        out = torch.empty((T, O), dtype=out_dtype, device=a.device)
+    else:
+        _check_output("out", out, T * O * out_dtype.itemsize, a.device, out_dtype)
+    if status is not None:
+        _check_output("status", status, 4, a.device, torch.int32)
+    _lib.check(lib.fq_int8_matmul(T, O, L, _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _OUT_DT[out_dtype],
+                                  _ptr(out), _ptr(status), _stream_ptr(stream)), "fq_int8_matmul")
+    return out
+
+
+class KVCache:
+    """A paged key / value cache in 8 bits: E4M3 codes [num_pages, kv_heads, page_size, head_dim]
+    (`k`, `v`) and one E8M0 byte for each page and head, [num_pages, kv_heads] (`k_scale`,
+    `v_scale`); see fq_kv_cache. page_size 16, 32, 64 or 128, head_dim 64 or 128.
+
+    The batch of a call is given by three int32 CUDA tensors, which the kernels read on the
+    device: cu_new [B + 1] (rows cu_new[b] .. cu_new[b + 1] - 1 of the token arrays are sequence
+    b's new tokens), seq_lens [B] (lengths with the new tokens) and page_table [B, W].
+    """
+
+    def __init__(self, num_pages, page_size, kv_heads, head_dim, device=None):
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        shape = (int(num_pages), int(kv_heads), int(page_size), int(head_dim))
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.full(shape[:2], 87, dtype=torch.uint8, device=dev) for _ in range(2)]
+        self._attach(*codes, *scales)
+
+    @classmethod
+    def from_buffers(cls, k, v, k_scale, v_scale):
+        """A cache over the caller's own tensors (k, v float8_e4m3fn, the scales uint8)."""
+        self = cls.__new__(cls)
+        self._attach(k, v, k_scale, v_scale)
+        return self
+
+    def _attach(self, k, v, k_scale, v_scale):
+        for name, t, dt in (("k", k, torch.float8_e4m3fn), ("v", v, torch.float8_e4m3fn),
+                            ("k_scale", k_scale, torch.uint8), ("v_scale", v_scale, torch.uint8)):
+            _check_input(name, t, dt)
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must both be [num_pages, kv_heads, page_size, head_dim]")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.shape != k.shape[:2]:
+                raise ValueError(f"{name} must be [num_pages, kv_heads]")
+        for name, t in (("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.device != k.device:
+                raise ValueError(f"{name} must be on {k.device}, got {t.device}")
+        if k.shape[2] not in (16, 32, 64, 128):
+            raise ValueError(f"page_size must be 16, 32, 64 or 128, got {k.shape[2]}")
+        if k.shape[3] not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {k.shape[3]}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self._status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._lib = _lib.load()
+
+    def device_status(self):
+        """Reads and clears the cache's status word: 0, or the bits that calls on this cache have
+        set since (FQ_KV_BAD_BATCH: a batch's contents were out of range). Synchronizes."""
+        v = int(self._status.item())
+        if v:
+            self._status.zero_()
+        return v
+
+    def _cache_desc(self):
+        return _lib.KvCacheDesc(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                                self.v_scale.data_ptr(), self.num_pages, self.kv_heads, self.page_size,
+                                self.head_dim)
+
+    def _batch_desc(self, cu_new, seq_lens, page_table):
+        for name, t in (("cu_new", cu_new), ("seq_lens", seq_lens), ("page_table", page_table)):
+            _check_input(name, t, torch.int32)
+        B = seq_lens.numel()
+        if seq_lens.dim() != 1 or cu_new.dim() != 1 or cu_new.numel() != B + 1:
+            raise ValueError("seq_lens must be [B] and cu_new [B + 1]")
+        if page_table.dim() != 2 or page_table.shape[0] != B:
+            raise ValueError("page_table must be [B, W]")
+        return _lib.KvBatchDesc(cu_new.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), B,
+                                page_table.shape[1])
+
+    def _tokens(self, name, t, T, heads, dtype):
+        """A token array [T, heads, head_dim]: heads contiguous, any distance between tokens."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (libfq has no CPU path)")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+        D = self.head_dim
+        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+            raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
+        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+            raise ValueError(f"the heads of one token of {name} must be contiguous")
+        return t.stride(0) if T > 1 else t.shape[1] * D
+
+    def append(self, k, v, cu_new, seq_lens, page_table, q=None, inv_freq=None, interleaved=False, q_out=None,
+               stream=None):
+        """Appends k and v [T, kv_heads, head_dim] (bfloat16 or float16) to the cache. With
+        inv_freq (float32 [rot / 2]) keys, and q [T, q_heads, head_dim] if given, are rotated by
+        their positions first (see fq_kv_append). Returns the rotated queries, or None."""
+        if not isinstance(k, torch.Tensor) or k.dtype not in _DT:
+            raise ValueError("k must be a bfloat16 or float16 tensor")
+        T = k.shape[0]
+        ks = self._tokens("k", k, T, self.kv_heads, k.dtype)
+        vs = self._tokens("v", v, T, self.kv_heads, k.dtype)
+        batch = self._batch_desc(cu_new, seq_lens, page_table)
+        rot, qs, hq = 0, 0, 0
+        if inv_freq is not None:
+            _check_input("inv_freq", inv_freq, torch.float32)
+            rot = 2 * inv_freq.numel()
+        if q is not None:
+            qs = self._tokens("q", q, T, None, k.dtype)
+            hq = q.shape[1]
+        _check_device(k, cache=self.k, v=v, q=q, cu_new=cu_new, seq_lens=seq_lens, page_table=page_table,
+                      inv_freq=inv_freq)
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out needs q")
+        elif q_out is None:
+            q_out = torch.empty((T, hq, self.head_dim), dtype=q.dtype, device=q.device)
+        else:
+            _check_output("q_out", q_out, T * hq * self.head_dim * 2, q.device, q.dtype)
+        cache = self._cache_desc()
+        _lib.check(self._lib.fq_kv_append(
+            ctypes.byref(cache), ctypes.byref(batch), T, _DT[k.dtype], _ptr(k), ks, _ptr(v), vs, _ptr(inv_freq), rot,
+            int(bool(interleaved)), _ptr(q), qs, hq, _ptr(q_out), _ptr(self._status), _stream_ptr(stream)),
+            "fq_kv_append")
+        return q_out
+
+    def attention(self, q, cu_new, seq_lens, page_table, max_q_len, max_seq_len=None, scale=None, causal=True,
+                  out=None, lse=None, return_lse=False, stream=None):
+        """softmax(scale q k^T) v over the cache for the new tokens' queries q [T, q_heads,
+        head_dim] (see fq_kv_attention). max_q_len and max_seq_len bound the batch's new tokens
+        and lengths (max_seq_len: the page table's capacity unless given); scale: head_dim ** -0.5
+        unless given. Returns out, or (out, lse [T, q_heads] float32) with return_lse."""
+        if not isinstance(q, torch.Tensor) or q.dtype not in _DT:
+            raise ValueError("q must be a bfloat16 or float16 tensor")
+        T = q.shape[0]
+        qs = self._tokens("q", q, T, None, q.dtype)
+        hq, D = q.shape[1], self.head_dim
+        batch = self._batch_desc(cu_new, seq_lens, page_table)
+        _check_device(q, cache=self.k, cu_new=cu_new, seq_lens=seq_lens, page_table=page_table)
+        if max_seq_len is None:
+            max_seq_len = page_table.shape[1] * self.page_size
+        if out is None:
+            out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+        else:
+            _check_output("out", out, T * hq * D * 2, q.device, q.dtype)
+        if lse is not None:
+            _check_output("lse", lse, T * hq * 4, q.device, torch.float32)
+        elif return_lse:
+            lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+        cache = self._cache_desc()
+        need = ctypes.c_int64(0)
+        _lib.check(self._lib.fq_kv_attention_workspace(ctypes.byref(cache), ctypes.byref(batch), T, hq, int(max_q_len),
+                                                       int(max_seq_len), ctypes.byref(need)),
+                   "fq_kv_attention_workspace")
+        ws = None
+        if need.value:
+            ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+            if stream is not None:
+                ws.record_stream(stream)  # freed on this stream's clock, used on the other's
+        _lib.check(self._lib.fq_kv_attention(
+            ctypes.byref(cache), ctypes.byref(batch), T, _DT[q.dtype], _ptr(q), qs, hq, int(max_q_len),
+            int(max_seq_len), float(scale if scale is not None else D ** -0.5), int(bool(causal)), _ptr(out), _ptr(lse),
+            _ptr(ws), need.value, _ptr(self._status), _stream_ptr(stream)), "fq_kv_attention")
+        return (out, lse) if return_lse else out
+
+
 def debug_rotate(x, P1, P2, kernel="auto"):
     K, M, N = x.shape
     return FlatQuant(K, M, N, x.dtype, kernel).debug_rotate(x, P1, P2)
@@ -267,7 +461,9 @@ class HostPipeline:
         self.P1 = torch.empty((M, M), dtype=fq.dtype, device=dev)
         self.P2 = torch.empty((N, N), dtype=fq.dtype, device=dev)
         if mode == "per_token":
-            if out_dtype == "int32":
+            if out_dtype == "int8":
+                self.out = torch.empty((K, M * N), dtype=torch.int8, device=dev)
+            elif out_dtype == "int32":
                 self.out = torch.empty((K, M, N // 8), dtype=torch.int32, device=dev)
             else:
                 self.out = torch.empty((K, M * N // 2), dtype=torch.uint8, device=dev)

@@ -155,14 +155,14 @@ fq_status fq_quantize_per_token(fq_handle* h, const void* x, const void* P1, con
     if (h->N % 2 != 0) return FQ_ERR_INVALID;
   } else if (fmt == FQ_OUT_INT32) {
     if (h->N % 8 != 0 || !aligned(out, 4)) return FQ_ERR_INVALID;
-  } else {
+  } else if (fmt != FQ_OUT_INT8) {
     return FQ_ERR_INVALID;
   }
   if (!aligned(x, 2) || !aligned(P1, 2) || !aligned(P2, 2) || !aligned(quantScale, 4))
     return FQ_ERR_INVALID;
   fq::MxRule rule{fq::kMxFloor, 0.0f, 0.0f};
-  return launch(h, fq::kModePerToken, x, P1, P2, clipRatio, rule, static_cast<uint8_t*>(out),
-                quantScale, nullptr, nullptr, reinterpret_cast<cudaStream_t>(stream));
+  return launch(h, fmt == FQ_OUT_INT8 ? fq::kModePerToken8 : fq::kModePerToken, x, P1, P2, clipRatio, rule,
+                static_cast<uint8_t*>(out), quantScale, nullptr, nullptr, reinterpret_cast<cudaStream_t>(stream));
 }
 
 fq_status fq_quantize_mx(fq_handle* h, const void* x, const void* P1, const void* P2,
@@ -208,6 +208,24 @@ fq_status fq_mx_matmul(int64_t T, int64_t O, int64_t L, const void* a_fp4, const
   if (e != cudaSuccess) return cuda_fail(e);
   fq::MxGemmParams p{a_fp4, a_scale_e8m0, w_fp4, w_scale_e8m0, C, status, T, O, L};
   e = fq::launch_mxgemm(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FQ_OK : cuda_fail(e);
+}
+
+fq_status fq_int8_matmul(int64_t T, int64_t O, int64_t L, const int8_t* a, const float* a_scale, const int8_t* w,
+                         const float* w_scale, fq_dtype out_type, void* C, uint32_t* status,
+                         struct CUstream_st* stream) {
+  if (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || C == nullptr) return FQ_ERR_NULLPTR;
+  if (out_type != FQ_BF16 && out_type != FQ_FP16 && out_type != FQ_FP32) return FQ_ERR_INVALID;
+  if (T < 1 || T > 262144 || O < 1 || O > 262144 || L < 16 || L > 65536 || L % 16 != 0) return FQ_ERR_INVALID;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
+      !aligned(C, out_type == FQ_FP32 ? 4 : 2) || (status && !aligned(status, 4)))
+    return FQ_ERR_INVALID;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  fq::I8GemmParams p{a, a_scale, w, w_scale, C, status, T, O, L, out_type};
+  e = fq::launch_i8gemm(p, sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FQ_OK : cuda_fail(e);
 }
 

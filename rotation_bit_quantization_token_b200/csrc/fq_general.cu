@@ -75,6 +75,7 @@ general_kernel(const GeneralParams p) {
   const T* __restrict__ P1 = static_cast<const T*>(p.P1);
   const T* __restrict__ P2 = static_cast<const T*>(p.P2);
   const int passes = (p.mode == kModeRotate) ? 1 : 2;
+  const bool per_token = p.mode == kModePerToken || p.mode == kModePerToken8;
 
   for (int64_t k = blockIdx.x; k < p.K; k += gridDim.x) {
     const T* __restrict__ xk = static_cast<const T*>(p.x) + k * MN;
@@ -121,14 +122,16 @@ general_kernel(const GeneralParams p) {
             if (valid) p.x2[k * MN + f] = acc;
           } else if (pass == 0) {
             if (valid) {
-              if (p.mode == kModePerToken) tmax = fmaxf(tmax, fabsf(acc));
+              if (per_token) tmax = fmaxf(tmax, fabsf(acc));
               else atomicMax(&gmax[f >> 5], __float_as_uint(fabsf(acc)));
             }
           } else {
             // encode; lanes (c, c+1) hold flat elements (f, f+1) because cb and N are even
-            float v = (p.mode == kModePerToken) ? acc * s_inv_scale : acc * gR[valid ? (f >> 5) : 0];
+            float v = per_token ? acc * s_inv_scale : acc * gR[valid ? (f >> 5) : 0];
             const float v_hi = __shfl_down_sync(0xffffffffu, v, 1);
-            if (valid && (c & 1) == 0) {
+            if (p.mode == kModePerToken8) {
+              if (valid) p.out[k * MN + f] = uint8_t(int8_byte(v));  // no pairs: any N
+            } else if (valid && (c & 1) == 0) {
               uint32_t byte;
               if (p.mode == kModePerToken) byte = int4_nibble(v) | (int4_nibble(v_hi) << 4);
               else byte = e2m1_canonical_zero(e2m1x2_raw(v, v_hi));
@@ -139,14 +142,14 @@ general_kernel(const GeneralParams p) {
         __syncthreads();
       }
 
-      if (pass == 0 && p.mode == kModePerToken) {
+      if (pass == 0 && per_token) {
         tmax = warp_max(tmax);
         if (lane == 0) red[tid >> 5] = tmax;
         __syncthreads();
         if (tid == 0) {
           float a = 0.0f;
           for (int w = 0; w < kThreads / 32; ++w) a = fmaxf(a, red[w]);
-          const float qs = per_token_scale(a, p.clip_ratio);
+          const float qs = per_token_scale(a, p.clip_ratio, p.mode == kModePerToken8 ? 127.0 : 7.0);
           p.quant_scale[k] = qs;
           s_inv_scale = (qs > 0.0f) ? __frcp_rn(qs) : 0.0f;
         }

@@ -5,11 +5,12 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "fq.h"
 #include "fq_quant.cuh"
 
 namespace fq {
 
-enum Mode : int { kModePerToken = 0, kModeMx = 1, kModeRotate = 2 };
+enum Mode : int { kModePerToken = 0, kModeMx = 1, kModeRotate = 2, kModePerToken8 = 3 /* INT8 codes */ };
 
 struct GeneralParams {
   const void* x;       // [K, M, N] 16-bit
@@ -20,7 +21,7 @@ struct GeneralParams {
   int mode;            // Mode
   double clip_ratio;   // per-token
   MxRule rule;         // per-group
-  uint8_t* out;        // packed codes, K*M*N/2 bytes
+  uint8_t* out;        // packed codes, K*M*N/2 bytes (INT8: K*M*N bytes)
   float* quant_scale;  // [K] per-token
   uint8_t* scales;     // [K, 2*ceilDiv(M*N,64)] per-group
   float* x2;           // [K, M, N] rotate-only
@@ -69,6 +70,19 @@ struct MxGemmParams {
   int64_t T, O, L;
 };
 cudaError_t launch_mxgemm(const MxGemmParams& p, int num_sms, cudaStream_t stream);
+
+// INT8 x INT8 product with a scale per row of each operand (see fq_i8gemm.cu).
+struct I8GemmParams {
+  const void* a;         // [T, L] int8, 16-byte aligned, L % 16 == 0
+  const float* a_scale;  // [T]
+  const void* w;         // [O, L] int8
+  const float* w_scale;  // [O]
+  void* C;               // [T, O] of out_type
+  uint32_t* status;      // bounded-wait status word, or nullptr
+  int64_t T, O, L;
+  fq_dtype out_type;
+};
+cudaError_t launch_i8gemm(const I8GemmParams& p, int num_sms, cudaStream_t stream);
 
 // Keeps a CUDA error code for fq_last_cuda_error() (thread-local).
 void record_cuda_error(int e);

@@ -1,0 +1,54 @@
+// Internal declarations of the 8-bit paged cache: argument blocks shared by the host layer
+// (fq_kv_api.cu) and the kernels (fq_kv_append.cu, fq_kv_attn.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fq.h"
+
+namespace fq {
+
+constexpr int kPageExpMin = -40, kPageExpMax = 40;  // range of a page's shared exponent
+
+struct KvAppendParams {
+  fq_kv_cache c;
+  fq_kv_batch b;
+  const void* k;
+  const void* v;
+  const void* q;
+  void* q_out;
+  const float* inv_freq;
+  uint32_t* status;
+  int64_t T, k_stride, v_stride, q_stride;
+  int rot_dim, interleaved, q_heads;
+  int heads_per_cta;  // key / value heads of one CTA
+};
+cudaError_t launch_kv_append(const KvAppendParams& p, bool fp16, int num_sms, cudaStream_t stream);
+
+struct KvAttnParams {
+  fq_kv_cache c;
+  fq_kv_batch b;
+  const void* q;
+  void* out;
+  float* lse;
+  float* ws;         // partial results: [T * q_heads, splits, head_dim + 2]
+  uint32_t* status;
+  int64_t T, q_stride, max_seq_len;
+  int q_heads, max_q_len, causal, fp16;
+  float scale;
+  int chunk;         // keys of one split
+  int splits;        // splits of the longest sequence
+};
+
+// How fq_kv_attention divides its work; the workspace follows from it.
+struct KvAttnPlan {
+  int chunk, splits, row_tiles;
+  int64_t ws_bytes;
+};
+KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, int q_heads, int max_q_len,
+                        int64_t max_seq_len, int num_sms);
+cudaError_t launch_kv_attn(const KvAttnParams& p, const KvAttnPlan& plan, int num_sms, cudaStream_t stream);
+
+}  // namespace fq

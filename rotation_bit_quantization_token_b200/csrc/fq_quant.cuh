@@ -153,9 +153,17 @@ __device__ __forceinline__ uint32_t int4_nibble(float v) {
   return uint32_t(q) & 0xFu;
 }
 
-// quantScale = fp32(amax / (7 / clipRatio)), the division taken in double.
-__device__ __forceinline__ float per_token_scale(float amax, double clip_ratio) {
-  return float(double(amax) / (7.0 / clip_ratio));
+// INT8 code: round half to even, clamp to [-128, 127].
+__device__ __forceinline__ uint32_t int8_byte(float v) {
+  int q = __float2int_rn(v);
+  q = q < -128 ? -128 : (q > 127 ? 127 : q);
+  return uint32_t(q) & 0xFFu;
+}
+
+// quantScale = fp32(amax / (top / clipRatio)), the division taken in double; top is the
+// largest code (7 for INT4, 127 for INT8).
+__device__ __forceinline__ float per_token_scale(float amax, double clip_ratio, double top = 7.0) {
+  return float(double(amax) / (top / clip_ratio));
 }
 
 }  // namespace fq

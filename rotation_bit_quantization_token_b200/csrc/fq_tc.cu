@@ -69,7 +69,9 @@ enum : uint32_t {
   kStMmaDone = 1u << 6, kStDrain = 1u << 7
 };
 
-template <int N>
+// kBits: bits of an output code (4, or 8 for INT8 codes, whose staging buffers are twice as
+// large: a stage or more of the x ring makes room for them)
+template <int N, int kBits = 4>
 struct Geo {
   static_assert(N % 16 == 0 && N >= 64 && N <= 128, "tensor-core kernel covers N in [64,128], N % 16 == 0");
   static constexpr int kAtoms = (N + 63) / 64;              // 64-element swizzle atoms along N
@@ -78,7 +80,8 @@ struct Geo {
   // another at 128 x 112: the loads land well ahead), four at N = 64 (eight measured
   // slower: the longer first round of loads delays the first tile), three at N = 128
   // where BD(P1) stays in shared memory
-  static constexpr int kStages = N == 128 ? 3 : (N == 64 ? 4 : 5);
+  static constexpr int kStages = kBits == 4 ? (N == 128 ? 3 : (N == 64 ? 4 : 5))
+                                            : (N == 128 ? 2 : (N == 80 ? 5 : 4));
   // BD(P1) sits in TMEM (64 columns; stage A is then a TS MMA that reads only the x tile
   // from shared memory, 3.5 KB instead of 7.5 KB per MMA at N = 112) when four N-column
   // slots still fit beside it; otherwise in shared memory, 128 x 128, two K atoms (SS).
@@ -86,8 +89,8 @@ struct Geo {
   static constexpr uint32_t kP1Col = 448;                   // its first TMEM column
   static constexpr int kP1Bytes = kP1Tmem ? 0 : 2 * 128 * 128;
   static constexpr int kP2Bytes = kAtoms * N * 128;         // P2^T: N rows, kAtoms K atoms
-  static constexpr int kCodeBytes = 128 * N / 2;
-  static constexpr int kScaleBytes = 4 * N;                 // 128 rows x N/32 groups
+  static constexpr int kCodeBytes = 128 * N * kBits / 8;
+  static constexpr int kScaleBytes = kBits == 4 ? 4 * N : 0;  // 128 rows x N/32 groups (per-group modes)
   static constexpr int kOutStride = (kCodeBytes + kScaleBytes + 1023) & ~1023;
   static constexpr int kOffP1 = 0;
   static constexpr int kOffP2 = kOffP1 + kP1Bytes;
@@ -134,7 +137,7 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 4096, "barrier block");
 template <int N>
-constexpr bool smem_fits() { return Geo<N>::kSmem <= 232448; }  // 227 KB opt-in per block
+constexpr bool smem_fits() { return Geo<N>::kSmem <= 232448 && Geo<N, 8>::kSmem <= 232448; }  // 227 KB opt-in per block
 static_assert(smem_fits<64>() && smem_fits<80>() && smem_fits<96>() && smem_fits<112>() && smem_fits<128>(),
               "shared memory");
 
@@ -455,7 +458,7 @@ __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cas
 template <int N, bool kF16, int kMode, bool kRatio>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_kernel(const __grid_constant__ CUtensorMap tmap, const TcParams p) {
-  using G = Geo<N>;
+  using G = Geo<N, kMode == kModePerToken8 ? 8 : 4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + G::kOffBar);
@@ -860,11 +863,26 @@ tc_kernel(const __grid_constant__ CUtensorMap tmap, const TcParams p) {
           for (int c = 0; c < nbk; ++c) {
             const int sg = c0 + c;
             const float2 F2 = make_float2(Fseg[sg], Fseg[sg]);
-            uint32_t words[2];
+            uint32_t words[2] = {0u, 0u};
+            uint32_t words8[4];  // INT8 codes
 #pragma unroll
             for (int wd = 0; wd < 2; ++wd) {
               const float* w = d + c * 16 + wd * 8;
-              if constexpr (kMode == kModePerToken) {
+              if constexpr (kMode == kModePerToken8) {
+                // eight codes: two words of four, each packed (saturated to [-128, 127]) from
+                // its highest pair down
+#pragma unroll
+                for (int hw = 0; hw < 2; ++hw) {
+                  uint32_t acc = 0u;
+#pragma unroll
+                  for (int e = 2; e >= 0; e -= 2) {
+                    const float2 t = __fmul2_rn(make_float2(w[4 * hw + e], w[4 * hw + e + 1]), F2);
+                    const int lo = __float2int_rn(t.x), hi = __float2int_rn(t.y);
+                    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(acc) : "r"(hi), "r"(lo), "r"(acc));
+                  }
+                  words8[2 * wd + hw] = acc;
+                }
+              } else if constexpr (kMode == kModePerToken) {
                 // integer nearest (ties to even), then clamped to [-8, 7] and packed by the
                 // saturating pack: it puts its second operand in the low nibble, its first
                 // above it, and the carried word above both, so the highest pair goes first
@@ -884,7 +902,11 @@ tc_kernel(const __grid_constant__ CUtensorMap tmap, const TcParams p) {
                 words[wd] = e2m1_canonical_zero(e2m1x8(a, b, cc, dd));
               }
             }
-            *reinterpret_cast<uint2*>(s_out + row * (N / 2) + sg * 8) = make_uint2(words[0], words[1]);
+            if constexpr (kMode == kModePerToken8)
+              *reinterpret_cast<uint4*>(s_out + row * N + sg * 16) =
+                  make_uint4(words8[0], words8[1], words8[2], words8[3]);
+            else
+              *reinterpret_cast<uint2*>(s_out + row * (N / 2) + sg * 8) = make_uint2(words[0], words[1]);
           }
         }
       };
@@ -925,7 +947,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmap, const TcParams p) {
         }
         if (leader) bulk_wait_read<0>();  // this group's previous store has left the staging buffer
         float Fseg[NS];
-        if constexpr (kMode == kModePerToken) {
+        if constexpr (kMode == kModePerToken || kMode == kModePerToken8) {
           float rmax = 0.0f;
 #pragma unroll
           for (int sg = 0; sg < NS; ++sg) rmax = fmaxf(rmax, smax[sg]);
@@ -935,7 +957,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmap, const TcParams p) {
           float amax = 0.0f;
           const int q0 = (tok_in_tile * M) >> 5, nq = (M + 31) >> 5;
           for (int qq = 0; qq < nq; ++qq) amax = fmaxf(amax, bars->red[eg][q0 + qq]);
-          const float qs = per_token_scale(amax, p.clip_ratio);
+          const float qs = per_token_scale(amax, p.clip_ratio, kMode == kModePerToken8 ? 127.0 : 7.0);
           const float inv = qs > 0.0f ? __frcp_rn(qs) : 0.0f;
           if (row_valid && m_row == 0) p.quant_scale[grow / M] = qs;
 #pragma unroll
@@ -1020,7 +1042,8 @@ tc_kernel(const __grid_constant__ CUtensorMap tmap, const TcParams p) {
         named_bar(bar_id, 128);
         if (leader) {
           const int64_t row0 = int64_t(tile) * 128;
-          bulk_store(p.out + row0 * (N / 2), s_out_u32, uint32_t(valid_rows * (N / 2)));
+          constexpr int kRow = G::kCodeBytes / 128;  // code bytes of a row
+          bulk_store(p.out + row0 * kRow, s_out_u32, uint32_t(valid_rows * kRow));
           if constexpr (kMode == kModeMx)
             bulk_store(p.scales + (row0 * N) / 32, s_out_u32 + G::kCodeBytes, uint32_t((valid_rows * N) / 32));
           bulk_commit();
@@ -1057,7 +1080,7 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 
 template <int N, bool kF16, int kMode, bool kRatio = false>
 cudaError_t launch_n(const TcParams& p, int num_sms, cudaStream_t stream) {
-  using G = Geo<N>;
+  using G = Geo<N, kMode == kModePerToken8 ? 8 : 4>;
   auto enc = get_encode();
   if (enc == nullptr) return cudaErrorNotSupported;
   CUtensorMap map;
@@ -1089,6 +1112,8 @@ template <int N>
 cudaError_t launch_mode(const TcParams& p, bool f16, int sms, cudaStream_t s) {
   if (p.mode == kModePerToken)
     return f16 ? launch_n<N, true, kModePerToken>(p, sms, s) : launch_n<N, false, kModePerToken>(p, sms, s);
+  if (p.mode == kModePerToken8)
+    return f16 ? launch_n<N, true, kModePerToken8>(p, sms, s) : launch_n<N, false, kModePerToken8>(p, sms, s);
   if (p.mode == kModeMx)
   {
     if (p.rule.mode == kMxRatio)
