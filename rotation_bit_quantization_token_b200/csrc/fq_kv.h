@@ -40,15 +40,23 @@ struct KvAttnParams {
   float scale;
   int chunk;         // keys of one split
   int splits;        // splits of the longest sequence
+  int64_t tc_rows;   // sequences with more rows (new tokens * group) take the tensor-core kernel
+  int tc_chunk, tc_splits;
+  int ws_splits;     // slots per row of the workspace: max(splits, tc_splits)
 };
 
 // How fq_kv_attention divides its work; the workspace follows from it.
 struct KvAttnPlan {
-  int chunk, splits, row_tiles;
+  int chunk, splits, row_tiles;             // mma.sync kernel: 16 rows and one chunk per CTA; 0 row tiles: not launched
+  int tc_chunk, tc_splits, tc_row_tiles;    // tensor-core kernel: 256 rows and one chunk per CTA; 0: not launched
+  int64_t tc_rows;
   int64_t ws_bytes;
 };
 KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, int q_heads, int max_q_len,
                         int64_t max_seq_len, int num_sms);
-cudaError_t launch_kv_attn(const KvAttnParams& p, const KvAttnPlan& plan, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_attn(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_t stream);
+cudaError_t launch_kv_attn_tc(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_t stream);
+
+constexpr int kTcRows = 256;  // rows of a CTA of the tensor-core kernel
 
 }  // namespace fq

@@ -21,25 +21,20 @@
 // units of the page's own scale of v and moves to the next page's unit by a power of two, so
 // that no page's scale has to fit beside another's in fp16: exponents lie in [-40, 40], so a
 // unit changes by at most 2^80 and float32 holds all of it.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <cstdint>
 
-#include "fq_kv.h"
-#include "fq_ptx.cuh"
+#include "fq_kv_common.cuh"
 
 namespace fq {
 namespace {
 
 using namespace ptx;
+using namespace kv;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTileKeys = 32;   // keys of one warp's step
 constexpr int kRowsTile = 16;   // rows of a CTA
 constexpr int kMaxChunk = 8192; // keys of a chunk (its page numbers sit in shared memory)
-constexpr float kLog2e = 1.4426950408889634f;
-
 enum : uint32_t { kStFull = 1u << 0 };
 
 template <int D>
@@ -57,22 +52,6 @@ struct Shared {
   float m[kWarps][kRowsTile], l[kWarps][kRowsTile];
   int abort;
 };
-
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Codes in bytes 1 and 3 of w as two fp16 numbers (code * 2^-8): sign to bit 15, the seven
-// bits below it to bits 13 .. 7.
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
-  return (w & 0x80008000u) | ((w >> 1) & 0x3F803F80u);
-}
-// The same for bytes 0 and 2 (the shifts as multiplications, which run beside the logic).
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
-  return (w & 0x00800080u) * 256u + (w & 0x007F007Fu) * 128u;
-}
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -98,36 +77,6 @@ __device__ __forceinline__ uint32_t swz(int key, int d) {
   return o ^ (((o >> 7) & 7u) << 4);
 }
 
-__device__ __forceinline__ uint32_t h2(float a, float b) {
-  const __half2 v = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// One sequence's rows [row0, row0 + 16) and the keys they can see.
-struct Rows {
-  int64_t t_first;  // first token row of the sequence
-  int64_t n, len;   // new tokens, length
-  int64_t end;      // keys seen by at least one row of the tile
-  bool ok;
-};
-
-__device__ __forceinline__ Rows sequence_rows(const KvAttnParams& p, int b, int tile, int G) {
-  Rows r;
-  r.t_first = __ldg(p.b.cu_new + b);
-  r.n = int64_t(__ldg(p.b.cu_new + b + 1)) - r.t_first;
-  r.len = __ldg(p.b.seq_lens + b);
-  r.ok = r.n >= 0 && r.t_first >= 0 && r.t_first + r.n <= p.T;
-  r.ok = r.ok && r.len >= 0 && r.len <= p.max_seq_len && r.n <= r.len;
-  if (!r.ok) r.n = 0;
-  const int64_t last = min((int64_t(tile) * kRowsTile + kRowsTile - 1) / G, r.n - 1);
-  r.end = p.causal ? min(r.len, r.len - r.n + last + 1) : r.len;
-  if (r.end < 0) r.end = 0;
-  return r;
-}
-
-// p.q row of row index r (token r / G of the sequence, head h * G + r % G)
-__device__ __forceinline__ int64_t row_token(const Rows& s, int r, int G) { return s.t_first + r / G; }
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
 kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -150,12 +99,12 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   const int split = int(idx % p.splits);
   const int b = int(idx / p.splits);
 
-  const Rows s = sequence_rows(p, b, tile, G);
+  const Rows s = sequence_rows(p, b, int64_t(tile) * kRowsTile, kRowsTile, G);
   if (tid == 0 && split == 0 && h == 0 && tile == 0 && p.status != nullptr && (!s.ok || s.n > p.max_q_len))
     atomicOr(p.status, FQ_KV_BAD_BATCH);
   const int row0 = tile * kRowsTile;
   const int rows = int(min(int64_t(kRowsTile), s.n * G - row0));
-  if (rows <= 0) return;
+  if (rows <= 0 || takes_tc(p, s.n, G)) return;
   const int64_t c0 = int64_t(split) * p.chunk;  // first key of the chunk
   if (c0 >= s.end && split > 0) return;
   const int keys = int(min(int64_t(p.chunk), s.end - c0));
@@ -210,15 +159,12 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 
   for (int i = tid; i < n_pages; i += kThreads) {
     const int pg = s_page[i];
-    uint32_t kb = 127, vb = 127;
+    int ke = 0, ve = 0;
     if (pg >= 0) {
-      kb = __ldg(p.c.k_scale + int64_t(pg) * H + h);
-      vb = __ldg(p.c.v_scale + int64_t(pg) * H + h);
-      // a byte that fq_kv_append cannot have written still gives a number
-      kb = min(max(kb, uint32_t(127 + kPageExpMin)), uint32_t(127 + kPageExpMax));
-      vb = min(max(vb, uint32_t(127 + kPageExpMin)), uint32_t(127 + kPageExpMax));
+      ke = page_exp(__ldg(p.c.k_scale + int64_t(pg) * H + h));
+      ve = page_exp(__ldg(p.c.v_scale + int64_t(pg) * H + h));
     }
-    s_scale[i] = uint16_t(kb | (vb << 8));
+    s_scale[i] = uint16_t((ke + 127) | ((ve + 127) << 8));
   }
 
   // ---- q: this thread's elements of rows g and g + 8, t4 * D/4 .. + D/4 ----
@@ -231,7 +177,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     const bool live = g + 8 * hh < rows;
     float x[D / 4];
     float amax = 0.0f;
-    const int64_t base = live ? row_token(s, r, G) * p.q_stride + int64_t(h * G + r % G) * D + t4 * (D / 4) : 0;
+    const int64_t base = live ? (s.t_first + r / G) * p.q_stride + int64_t(h * G + r % G) * D + t4 * (D / 4) : 0;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
@@ -239,9 +185,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float2 f;
-        if (p.fp16) f = __half22float2(*reinterpret_cast<const __half2*>(&ww[e]));
-        else f = make_float2(__uint_as_float(ww[e] << 16), __uint_as_float(ww[e] & 0xFFFF0000u));
+        const float2 f = unpack16(ww[e], p.fp16);
         x[c * 8 + 2 * e] = f.x;
         x[c * 8 + 2 * e + 1] = f.y;
         amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
@@ -249,9 +193,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // largest magnitude to [2^14, 2^15); the exponent kept where 2^-qe and 2^qe are normal
-    int qe = int(__float_as_uint(amax) >> 23) - 127 - 14;
-    qe = min(max(qe, -100), 100);
+    const int qe = row_exponent(amax);
     const float f = exp2i(-qe);
 #pragma unroll
     for (int st = 0; st < kS; ++st) {
@@ -437,26 +379,18 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] += x[e] * f;
   }
-  const int64_t row = row_token(s, row0 + r, G) * p.q_heads + h * G + (row0 + r) % G;
+  const int64_t row = (s.t_first + (row0 + r) / G) * p.q_heads + h * G + (row0 + r) % G;
   if (whole) {
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     uint32_t w[kPer / 2];
 #pragma unroll
-    for (int e = 0; e < kPer / 2; ++e) {
-      const float a = acc[2 * e] * inv, c = acc[2 * e + 1] * inv;
-      if (p.fp16) {
-        w[e] = h2(a, c);
-      } else {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, c);
-        w[e] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-    }
+    for (int e = 0; e < kPer / 2; ++e) w[e] = pack16(acc[2 * e] * inv, acc[2 * e + 1] * inv, p.fp16);
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + d0);
 #pragma unroll
     for (int e = 0; e < kPer / 8; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-    if (p.lse != nullptr && (tid & 7) == 0) p.lse[row] = L > 0.0f ? (Mu + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    if (p.lse != nullptr && (tid & 7) == 0) p.lse[row] = L > 0.0f ? (Mu + log2f(L)) * kLn2 : -INFINITY;
   } else {
-    float* dst = p.ws + (row * p.splits + split) * (D + 4);
+    float* dst = p.ws + (row * p.ws_splits + split) * (D + 4);
 #pragma unroll
     for (int e = 0; e < kPer; e += 4)
       *reinterpret_cast<float4*>(dst + d0 + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
@@ -484,11 +418,13 @@ kv_attn_join_kernel(const KvAttnParams p) {
   }
   const int G = p.q_heads / p.c.kv_heads;
   const int64_t i = t - __ldg(p.b.cu_new + lo);
-  const int tile = int((i * G + hq % G) / kRowsTile);
-  const Rows s = sequence_rows(p, lo, tile, G);
-  if (i < 0 || i >= s.n || i >= p.max_q_len || s.end <= p.chunk) return;
-  const int n = int((s.end + p.chunk - 1) / p.chunk);
-  const float* src = p.ws + row * p.splits * (D + 4);
+  const int64_t n_new = int64_t(__ldg(p.b.cu_new + lo + 1)) - __ldg(p.b.cu_new + lo);
+  const bool tc = takes_tc(p, n_new, G);
+  const int tile_rows = tc ? kTcRows : kRowsTile, chunk = tc ? p.tc_chunk : p.chunk;
+  const Rows s = sequence_rows(p, lo, (i * G + hq % G) / tile_rows * tile_rows, tile_rows, G);
+  if (i < 0 || i >= s.n || i >= p.max_q_len || s.end <= chunk) return;
+  const int n = int((s.end + chunk - 1) / chunk);
+  const float* src = p.ws + row * p.ws_splits * (D + 4);
   float M = -INFINITY;
   for (int c = lane; c < n; c += 32) M = fmaxf(M, src[int64_t(c) * (D + 4) + D]);
 #pragma unroll
@@ -509,37 +445,45 @@ kv_attn_join_kernel(const KvAttnParams p) {
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
   uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    if (p.fp16) {
-      *reinterpret_cast<uint32_t*>(dst + e) = h2(acc[e] * inv, acc[e + 1] * inv);
-    } else {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-      *reinterpret_cast<uint32_t*>(dst + e) = *reinterpret_cast<const uint32_t*>(&v);
-    }
-  }
-  if (p.lse != nullptr && lane == 0) p.lse[row] = L > 0.0f ? (Mu + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack16(acc[e] * inv, acc[e + 1] * inv, p.fp16);
+  if (p.lse != nullptr && lane == 0) p.lse[row] = L > 0.0f ? (Mu + log2f(L)) * kLn2 : -INFINITY;
 }
 
 template <int D>
 cudaError_t launch_attn(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_t stream) {
-  const uint64_t rows128 = uint64_t(p.c.num_pages) * p.c.kv_heads * p.c.page_size * D / 128;
-  const int box = (p.c.page_size < kTileKeys ? p.c.page_size : kTileKeys) * D / 128;
-  CUtensorMap map_k, map_v;
-  if (!encode_bytes_2d(&map_k, p.c.k, rows128, 128, 128, uint32_t(box)) ||
-      !encode_bytes_2d(&map_v, p.c.v, rows128, 128, 128, uint32_t(box)))
-    return cudaErrorInvalidValue;
-  const int pages = (p.chunk + p.c.page_size - 1) / p.c.page_size;
-  const int smem = Geo<D>::kRing + int(sizeof(Shared)) + pages * 6 + 16 + 1024;
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t rows = p.T * p.q_heads;
-  const int64_t grid = int64_t(plan.row_tiles) * p.c.kv_heads * plan.splits * p.b.num_seqs;
-  if (grid > 0x7FFFFFFF || (rows + 3) / 4 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  kv_attn_kernel<D><<<unsigned(grid), kThreads, smem, stream>>>(map_k, map_v, p, plan.row_tiles);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || plan.splits == 1) return e;
-  kv_attn_join_kernel<D><<<unsigned((rows + 3) / 4), 128, 0, stream>>>(p);
+  if (plan.row_tiles > 0) {
+    const uint64_t rows128 = uint64_t(p.c.num_pages) * p.c.kv_heads * p.c.page_size * D / 128;
+    const int box = (p.c.page_size < kTileKeys ? p.c.page_size : kTileKeys) * D / 128;
+    CUtensorMap map_k, map_v;
+    if (!encode_bytes_2d(&map_k, p.c.k, rows128, 128, 128, uint32_t(box)) ||
+        !encode_bytes_2d(&map_v, p.c.v, rows128, 128, 128, uint32_t(box)))
+      return cudaErrorInvalidValue;
+    const int pages = (p.chunk + p.c.page_size - 1) / p.c.page_size;
+    const int smem = Geo<D>::kRing + int(sizeof(Shared)) + pages * 6 + 16 + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = int64_t(plan.row_tiles) * p.c.kv_heads * plan.splits * p.b.num_seqs;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    kv_attn_kernel<D><<<unsigned(grid), kThreads, smem, stream>>>(map_k, map_v, p, plan.row_tiles);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.ws_splits > 1) {
+    const int64_t blocks = (p.T * p.q_heads + 3) / 4;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    kv_attn_join_kernel<D><<<unsigned(blocks), 128, 0, stream>>>(p);
+  }
   return cudaGetLastError();
+}
+
+// Chunk of keys for `ctas` CTAs of one chunk each over max_len keys: chunks until there are
+// `want` CTAs, of at least `least` keys.
+int64_t chunk_for(int64_t max_len, int64_t ctas, int64_t want, int64_t least, int64_t most) {
+  const int64_t n = (want + ctas - 1) / ctas;
+  int64_t chunk = (max_len + n - 1) / n;
+  chunk = (chunk + 127) / 128 * 128;
+  return chunk < least ? least : (chunk > most ? most : chunk);
 }
 
 }  // namespace
@@ -548,22 +492,35 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
                         int64_t max_seq_len, int num_sms) {
   KvAttnPlan plan{};
   const int G = q_heads / c.kv_heads;
-  plan.row_tiles = int((int64_t(max_q_len) * G + kRowsTile - 1) / kRowsTile);
-  // chunks until the CTAs fill the machine twice over, of at least 256 keys
-  const int64_t ctas = int64_t(b.num_seqs) * c.kv_heads * plan.row_tiles;
-  const int64_t want = (int64_t(num_sms) * 4 + ctas - 1) / ctas;
-  int64_t chunk = (max_seq_len + want - 1) / want;
-  chunk = (chunk + 127) / 128 * 128;
-  if (chunk < 256) chunk = 256;
-  if (chunk > kMaxChunk) chunk = kMaxChunk;
-  plan.chunk = int(chunk);
-  plan.splits = int((max_seq_len + chunk - 1) / chunk);
-  plan.ws_bytes = plan.splits > 1 ? T * q_heads * plan.splits * int64_t(c.head_dim + 4) * 4 : 0;
+  const int64_t rows = int64_t(max_q_len) * G;  // of one sequence, at most
+  plan.tc_rows = 64;
+  const int64_t few = b.num_seqs == 1 && rows > plan.tc_rows ? 0 : (rows < plan.tc_rows ? rows : plan.tc_rows);
+  if (few == 0) plan.tc_rows = 0;  // one sequence: whatever its length, one kernel
+  plan.row_tiles = int((few + kRowsTile - 1) / kRowsTile);
+  plan.splits = plan.tc_splits = 1;
+  plan.chunk = plan.tc_chunk = 0x7FFFFF80;
+  if (plan.row_tiles > 0) {
+    const int64_t ctas = int64_t(b.num_seqs) * c.kv_heads * plan.row_tiles;
+    plan.chunk = int(chunk_for(max_seq_len, ctas, 4 * int64_t(num_sms), 256, kMaxChunk));
+    plan.splits = int((max_seq_len + plan.chunk - 1) / plan.chunk);
+  }
+  if (rows > plan.tc_rows) {
+    plan.tc_row_tiles = int((rows + kTcRows - 1) / kTcRows);
+    // the token rows bound the CTAs that have work, whatever the longest sequence
+    const int64_t tiles = (T * G + kTcRows - 1) / kTcRows;
+    plan.tc_chunk = int(chunk_for(max_seq_len, tiles * c.kv_heads, 2 * int64_t(num_sms), 1024, 1 << 24));
+    plan.tc_splits = int((max_seq_len + plan.tc_chunk - 1) / plan.tc_chunk);
+  }
+  const int64_t slots = plan.splits > plan.tc_splits ? plan.splits : plan.tc_splits;
+  plan.ws_bytes = slots > 1 ? T * q_heads * slots * int64_t(c.head_dim + 4) * 4 : 0;
   return plan;
 }
 
-cudaError_t launch_kv_attn(const KvAttnParams& p, const KvAttnPlan& plan, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
+cudaError_t launch_kv_attn(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_t stream) {
+  if (plan.tc_row_tiles > 0) {
+    const cudaError_t e = launch_kv_attn_tc(p, plan, stream);
+    if (e != cudaSuccess) return e;
+  }
   return p.c.head_dim == 128 ? launch_attn<128>(p, plan, stream) : launch_attn<64>(p, plan, stream);
 }
 

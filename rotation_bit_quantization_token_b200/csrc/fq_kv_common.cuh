@@ -1,0 +1,88 @@
+// What the two attention kernels over the 8-bit paged cache share: the rows of a sequence, the
+// conversion of codes, a row's final result.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "fq_kv.h"
+#include "fq_ptx.cuh"
+
+namespace fq {
+namespace kv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, int fp16) {
+  if (fp16) return h2(a, b);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two 16-bit elements as float32.
+__device__ __forceinline__ float2 unpack16(uint32_t w, int fp16) {
+  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Codes in bytes 1 and 3 of w as two fp16 numbers (code * 2^-8): sign to bit 15, the seven
+// bits below it to bits 13 .. 7. Every bit pattern gives a finite number.
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  return (w & 0x80008000u) | ((w >> 1) & 0x3F803F80u);
+}
+// The same for bytes 0 and 2 (the shifts as multiplications, which run beside the logic).
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  return (w & 0x00800080u) * 256u + (w & 0x007F007Fu) * 128u;
+}
+
+// Exponent qe such that amax * 2^-qe lies in [2^14, 2^15) (kept where 2^-qe and 2^qe are normal).
+__device__ __forceinline__ int row_exponent(float amax) {
+  const int e = int(__float_as_uint(amax) >> 23) - 127 - 14;
+  return min(max(e, -100), 100);
+}
+
+// Scale byte of a page as an exponent; a byte that fq_kv_append cannot have written still gives
+// a number.
+__device__ __forceinline__ int page_exp(uint32_t byte) {
+  return min(max(int(byte) - 127, kPageExpMin), kPageExpMax);
+}
+
+// The rows (new token, head of the group) row0 .. row0 + count - 1 of sequence b and the keys
+// that they can see.
+struct Rows {
+  int64_t t_first;  // first token row of the sequence
+  int64_t n, len;   // new tokens, length
+  int64_t end;      // keys seen by at least one of the rows
+  bool ok;
+};
+__device__ __forceinline__ Rows sequence_rows(const KvAttnParams& p, int b, int64_t row0, int count, int G) {
+  Rows r;
+  r.t_first = __ldg(p.b.cu_new + b);
+  r.n = int64_t(__ldg(p.b.cu_new + b + 1)) - r.t_first;
+  r.len = __ldg(p.b.seq_lens + b);
+  r.ok = r.n >= 0 && r.t_first >= 0 && r.t_first + r.n <= p.T;
+  r.ok = r.ok && r.len >= 0 && r.len <= p.max_seq_len && r.n <= r.len;
+  if (!r.ok) r.n = 0;
+  const int64_t last = min((row0 + count - 1) / G, r.n - 1);
+  r.end = p.causal ? min(r.len, r.len - r.n + last + 1) : r.len;
+  if (r.end < 0) r.end = 0;
+  return r;
+}
+
+// Whether the tensor-core kernel takes a sequence with n new tokens (else the other one does):
+// more than p.tc_rows rows. Both kernels and the join decide by it.
+__device__ __forceinline__ bool takes_tc(const KvAttnParams& p, int64_t n, int G) { return n * G > p.tc_rows; }
+
+}  // namespace kv
+}  // namespace fq

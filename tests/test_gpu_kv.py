@@ -516,3 +516,75 @@ def test_prompt_and_decode_steps_together():
     whole, parts = steps([n]), steps([30, 9, 1, 1, 1, 1, 1, 1])
     rms = whole.square().mean().sqrt()
     assert (whole - parts).square().mean().sqrt() < 2.0 ** -4 * rms  # one E4M3 step of keys and values
+
+
+# ------------------------------------------------------------------------------------
+# the tensor-core attention kernel (sequences with more than 64 rows)
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("n", [17, 64, 65, 127, 128, 129, 200, 257])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_row_tile_edges(n, D):
+    """Row counts around one and two row tiles of 128, alone and beside a decode step."""
+    for new, ctx in (([n], [0]), ([n, 1], [100, 40])):
+        s = Setup(new, ctx, H=1, D=D, page=64, seed=30).fill()
+        _check_attention(s, torch.bfloat16, G=1)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_key_step_edges(page, D, causal):
+    """Lengths around the 128-key steps, with pages that end inside one."""
+    s = Setup([70, 128, 90, 130], [1, 0, 167, 255], H=2, D=D, page=page, seed=31).fill()
+    _check_attention(s, torch.float16, G=2, causal=causal, strided=True)
+
+
+def test_attention_split_prompts():
+    """A short prompt on a long context is divided into chunks of keys and joined."""
+    s = Setup([40, 3], [5000, 2100], H=1, D=128, page=64, seed=32).fill()
+    _check_attention(s, torch.bfloat16, G=2)
+    s = Setup([90], [3000], H=1, D=64, page=16, seed=33).fill()
+    _check_attention(s, torch.float16, G=1)
+
+
+def test_attention_prompt_page_exponents():
+    """Pages whose exponents differ by up to 2^30 within one 128-key step."""
+    s = Setup([80], [300], H=1, D=128, page=16, seed=34).fill()
+    rng = np.random.default_rng(5)
+    for p in s.table[0]:
+        s.vs[p, 0] = 127 + rng.integers(-15, 16)
+        s.ks[p, 0] = min(s.ks[p, 0], 120) - rng.integers(0, 25)
+    _check_attention(s, torch.bfloat16, G=1)
+
+
+def test_attention_prompt_missing_page():
+    s = Setup([70], [200], H=1, D=64, page=16, seed=35).fill()
+    cache = s.cache()
+    q = torch.randn(70, 2, 64, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    cu, lens, table = s.batch()
+    t = table.clone()
+    t[0, 3] = s.pages + 5
+    out, lse = cache.attention(q, cu, lens, t, max_q_len=70, scale=0.125, return_lse=True)
+    assert cache.device_status() == _lib.FQ_KV_BAD_BATCH
+    k, v = osv.kv_values(s.k, s.ks, s.table[0], 270)[:, 0], osv.kv_values(s.v, s.vs, s.table[0], 270)[:, 0]
+    for i in (0, 33, 69):
+        keep = [j for j in range(200 + i + 1) if j // 16 != 3]
+        z = 0.125 * f64(q[i]) @ k[keep].T
+        assert np.allclose(f64(lse[i]), np.log(np.exp(z).sum(-1)), atol=1e-5)
+        p = np.exp(z) / np.exp(z).sum(-1, keepdims=True)
+        assert np.allclose(f64(out[i]), p @ v[keep], rtol=2.0 ** -7, atol=2e-3)
+
+
+def test_attention_loose_bounds():
+    """max_q_len and max_seq_len above what the batch has give the same result."""
+    s = Setup([70, 2, 1], [100, 300, 0], H=2, D=128, page=32, seed=36, width=100).fill()
+    cache = s.cache()
+    q = torch.randn(73, 4, 128, device="cuda").to(torch.bfloat16)
+    a = cache.attention(q, *s.batch(), max_q_len=70, max_seq_len=302)
+    b = cache.attention(q, *s.batch(), max_q_len=73, max_seq_len=3200)
+    assert (a.float() - b.float()).abs().max() <= 2.0 ** -6 * a.float().abs().max()
+    one = Setup([3], [50], H=1, D=64, page=16, seed=37).fill()
+    q = torch.randn(200, 2, 64, device="cuda").half()
+    a = one.cache().attention(q, *one.batch(), max_q_len=3)
+    b = one.cache().attention(q, *one.batch(), max_q_len=200)
+    assert (a[:3].float() - b[:3].float()).abs().max() <= 2.0 ** -9 * a[:3].float().abs().max()
