@@ -6,25 +6,25 @@
 //     S = Q K^T   (M = 128 rows, N = 128 keys, K = D; Q and K fp16 in shared memory)
 //     P = exp2(S c - m c)                      (registers, one thread per row)
 //     O += P V    (M = 128 rows, N = D, K = 128 keys; P fp16 in TMEM, V fp16 in shared memory)
-// The two row tiles take turns: while one's softmax runs, the tensor cores do the other's
-// products. Both share every converted tile of K and V.
+// The two row tiles take turns: while one's softmax runs, the tensor cores do the other's products.
+// Both share every converted tile of K and V.
 //
-// Codes reach the MMAs as fp16. A converter warpgroup moves the E4M3 bits into fp16 fields (every
-// bit pattern gives a finite number, so stale bytes behind the last token cannot make a NaN) and
-// multiplies by the page's power of two relative to the largest exponent among the sequence's
-// pages, times 2^14: codes of pages down to 2^-38 of the largest keep all their bits. One power of
-// two per row and one per output then undo all scaling: the score's factor c holds the softmax
-// scale, log2 e, the q row's exponent and the keys' largest page exponent.
+// Codes reach the MMAs as fp16, converted by a warpgroup that also multiplies by the page's power of
+// two relative to the largest exponent among the chunk's pages, times 2^6: codes of pages down to
+// 2^-21 of the largest keep all their bits. One power of two per row and one per output then undo
+// all scaling: the score's factor c holds the softmax scale, log2 e, the q row's exponent and the
+// keys' largest page exponent.
 //
 // Softmax. A thread owns one row (its TMEM lane), so no exchange is needed. The maximum that the
-// exponents are taken against is only raised when a row exceeds it by 2^8 (the probabilities then
-// stay below 2^8, within fp16, and relative rounding is the same): O and the sum are rescaled that
+// exponents are taken against is only raised when a row exceeds it by 2^15 (the probabilities then
+// stay below 2^15, within fp16, and relative rounding is the same): O and the sum are rescaled that
 // rarely. Probabilities are rounded to fp16 (2^-11).
 //
-// Roles, 512 threads: warps 0-3 and 4-7 softmax of row tile 0 and 1 (and its output), 8-11
-// converters, 12 TMA producer, 13 MMA issuer (owns TMEM). TMEM: O 2 x D columns, S 2 x 128 columns
-// (P overwrites the first half of its S). Every wait is bounded.
+// Roles, 512 threads: warps 0-3 and 4-7 softmax of row tile 0 and 1 (its Q before, its output
+// after), 8-11 converters, 12 TMA producer, 13 MMA issuer (owns TMEM). TMEM: O 2 x D columns, S
+// 2 x 128 columns (P overwrites the first half of its S). Every wait is bounded.
 #include <cstdint>
+#include <type_traits>
 
 #include "fq_kv_common.cuh"
 
@@ -34,28 +34,30 @@ namespace {
 using namespace ptx;
 using namespace kv;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kKeys = 128;  // keys of a step
 constexpr int kWarpConv0 = 8, kWarpProducer = 12, kWarpMma = 13;
 // Register split (setmaxnreg): launched at 128 per thread; 2 softmax warpgroups, the converters, the rest
-constexpr int kRegsSoftmax = 200, kRegsConv = 72, kRegsLow = 40;
-static_assert(128 * (2 * kRegsSoftmax + kRegsConv + kRegsLow) <= kThreads * 128, "register split");
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsConv = 72, kRegsLow = 40;
+static_assert(128 * (2 * kRegsSoftmax + kRegsConv + kRegsLow) <= kThreads * kRegsLaunch, "register split");
 
 enum : uint32_t {
-  kStRawFull = 1u << 0, kStRawEmpty = 1u << 1, kStKFull = 1u << 2, kStVFull = 1u << 3, kStKEmpty = 1u << 4,
-  kStVEmpty = 1u << 5, kStSFull = 1u << 6, kStPFull = 1u << 7, kStOFull = 1u << 9, kStDrain = 1u << 10
+  kStRawFull = 1u << 0, kStRawEmpty = 1u << 1, kStKFull = 1u << 2, kStVFull = 1u << 3, kStTEmpty = 1u << 4,
+    kStSFull = 1u << 6, kStPFull = 1u << 7, kStOFull = 1u << 9, kStDrain = 1u << 10, kStQFull = 1u << 11
 };
+
+constexpr uint32_t kAllThere = (1u << (kKeys / 16)) - 1u;  // a step with all its pages
 
 template <int D>
 struct Geo {
   static constexpr int kQBytes = 128 * D * 2;               // one row tile of Q
   static constexpr int kTile = kKeys * D * 2;               // a converted tile of K or V
   static constexpr int kRaw = kKeys * D;                    // its codes
-  static constexpr int kOffK = 2 * kQBytes;
-  static constexpr int kOffV = kOffK + 2 * kTile;
-  static constexpr int kOffRawK = kOffV + 2 * kTile;
-  static constexpr int kOffRawV = kOffRawK + kRaw;
-  static constexpr int kOffBars = kOffRawV + kRaw;
+  static constexpr int kTiles = 3;                          // ring of converted tiles, K and V in turn
+  static constexpr int kRaws = 4;                           // ring of code tiles
+  static constexpr int kOffTile = 2 * kQBytes;
+  static constexpr int kOffRaw = kOffTile + kTiles * kTile;
+  static constexpr int kOffBars = kOffRaw + kRaws * kRaw;
   static constexpr int kSmem = kOffBars + 1024 + 1024 /*alignment*/;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColO = 0, kColS = 2 * D, kCols = 512;
@@ -63,32 +65,78 @@ struct Geo {
 };
 
 struct Bars {
-  uint64_t raw_full[2], raw_empty[2];  // codes of K, of V
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  // unit u = 2j is K of step j, u = 2j + 1 V of step j
+  uint64_t raw_full[4], raw_empty[4];  // codes of unit u, slot u % 4
+  uint64_t t_full[3], t_empty[3];      // converted tile of unit u, slot u % 3
+  uint64_t s_full[2], p_full[2][2];  // row tile; P by halves of 64 keys
+  uint64_t o_full[2];                // row tile: O complete
+  uint64_t q_full;
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
-  int k_top, v_top;        // largest page exponents of the CTA's keys
-  uint32_t valid[8];       // per step (mod 8): pages of the step that are there, one bit per 16 keys
-  uint32_t factor[2][8];   // K, V: factor of each 16 keys of the step in the raw buffer, as half2
+  int k_top[kWarps], v_top[kWarps];  // largest page exponents of the CTA's keys, by warp
+  int8_t q_exp[kTcRows];   // exponents of Q's rows
+  // per step (mod 16; the producer is at most 4 + 3 steps ahead): the step's pages that are there, one
+  // bit per 16 keys
+  uint32_t valid[16];
+  uint32_t factor[4][8];   // per raw slot: factor of each 16 keys, as half2
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// One row tile's product under one election, the whole warp running the same code: descriptors then
+// stay in uniform registers. (A leader branch with one instruction per MMA took about 110 clocks
+// to issue each, twice what a 128 x 128 x 16 product needs.)
+//
+// S = Q K^T: D / 16 K steps, 32 bytes apart inside a 128-byte atom, atoms 128 rows of 128 bytes
+// apart (2 and 1024 in the descriptors' 16-byte units); the first overwrites S.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred f, t, e;\n\t.reg .b32 r;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "setp.ne.b32 f, %0, %0;\n\tsetp.eq.b32 t, %0, %0;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc)
+      : "memory");
+  if constexpr (D == 128)
+    asm volatile(
+        "{\n\t.reg .pred t, e;\n\t.reg .b32 r;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.eq.b32 t, %0, %0;\n\t"
+        "add.s64 a0, %1, 1024;\n\tadd.s64 a1, %1, 1026;\n\tadd.s64 a2, %1, 1028;\n\tadd.s64 a3, %1, 1030;\n\t"
+        "add.s64 b0, %2, 1024;\n\tadd.s64 b1, %2, 1026;\n\tadd.s64 b2, %2, 1028;\n\tadd.s64 b3, %2, 1030;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc)
+        : "memory");
+}
+// O += P V for 64 keys: four K steps of 16 (8 columns of P, 2048 bytes of V); acc = 0: the first overwrites.
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred f, t, e;\n\t.reg .b32 r, a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void commit_e(uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -121,9 +169,23 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+// Four codes as fp16 (the codes' values), in order: by the hardware conversion, or by moving bits
+// (finite for every pattern).
+__device__ __forceinline__ void cvt4(uint32_t w, uint32_t* y) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(y[0]), "=r"(y[1])
+      : "r"(w));
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void bits4(uint32_t w, uint32_t* y) {
+  const uint32_t k256 = 0x5C005C00u;  // codes_lo / codes_hi give code * 2^-8
+  const uint32_t lo = hmul2(codes_lo(w), k256), hi = hmul2(codes_hi(w), k256);
+  y[0] = __byte_perm(lo, hi, 0x5410);
+  y[1] = __byte_perm(lo, hi, 0x7632);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -131,7 +193,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-template <int D>
+template <int D, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1)
 kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   const KvAttnParams p, const int row_tiles) {
@@ -144,13 +206,13 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const int ps = p.c.page_size, H = p.c.kv_heads, G = p.q_heads / H;
 
   // the longest (last) row tiles first, so that the short ones fill the end of the launch
-  int64_t idx = blockIdx.x;
-  const int h = int(idx % H);
-  idx /= H;
-  const int b = int(idx % p.b.num_seqs);
-  idx /= p.b.num_seqs;
-  const int split = int(idx % p.tc_splits);
-  const int tile = row_tiles - 1 - int(idx / p.tc_splits);
+  unsigned idx = blockIdx.x;
+  const int h = int(idx % unsigned(H));
+  idx /= unsigned(H);
+  const int b = int(idx % unsigned(p.b.num_seqs));
+  idx /= unsigned(p.b.num_seqs);
+  const int split = int(idx % unsigned(p.tc_splits));
+  const int tile = row_tiles - 1 - int(idx / unsigned(p.tc_splits));
 
   const int64_t row0 = int64_t(tile) * kTcRows;
   const Rows s = sequence_rows(p, b, row0, kTcRows, G);
@@ -162,32 +224,56 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   if (c0 >= s.end && split > 0) return;
   const int keys = int(min(int64_t(p.tc_chunk), s.end - c0));
   const bool whole = s.end <= p.tc_chunk;
+  // row r of the CTA: token tok0 + (rem0 + r) / G of the array, head (rem0 + r) % G of the group (the
+  // one 64-bit division; a row's own is 32-bit)
+  const int64_t i0 = row0 / G;
+  const unsigned rem0 = unsigned(row0 - i0 * G), Gu = unsigned(G);
+  const int64_t tok0 = s.t_first + i0;
   const int n_steps = (keys + kKeys - 1) / kKeys;
   const int n_tiles = rows > 128 ? 2 : 1;  // row tiles with rows
   const int* table = p.b.page_table + int64_t(b) * p.b.table_width + c0 / ps;
   const int n_pages = (keys + ps - 1) / ps;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < G_::kRaws; ++i) {
       mbar_init(&bars->raw_full[i], 1);
       mbar_init(&bars->raw_empty[i], 4);
-      mbar_init(&bars->k_full[i], 4);
-      mbar_init(&bars->k_empty[i], 1);
-      mbar_init(&bars->v_full[i], 4);
-      mbar_init(&bars->v_empty[i], 1);
+    }
+    for (int i = 0; i < G_::kTiles; ++i) {
+      mbar_init(&bars->t_full[i], 4);
+      mbar_init(&bars->t_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < 2; ++k) mbar_init(&bars->p_full[i][k], 4);
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 4);
       mbar_init(&bars->o_full[i], 1);
     }
+    mbar_init(&bars->q_full, 4 * uint32_t(n_tiles));
     mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
-    bars->k_top = bars->v_top = kPageExpMin;
     fence_barrier_init();
   }
   if (warp == kWarpMma) tmem_alloc(&bars->tmem_base, G_::kCols);
-  __syncthreads();
+  // ---- Q on its way: kLpr lanes load a row, eight elements each; a softmax warp its own 32 rows ----
+  constexpr int kLpr = D / 8, kRpi = 32 / kLpr;  // lanes per row, rows per instruction
+  constexpr int kRowIter = 32 / kRpi;
+  const int c8 = lane % kLpr, sub = lane / kLpr;
+  uint4 qv[kRowIter];
+  int64_t my_row = 0;  // (token, head) index of this thread's row in q and out
+  if (warp < 4 * n_tiles) {
+    const unsigned ti = (rem0 + unsigned(tid)) / Gu, hi = rem0 + unsigned(tid) - ti * Gu;
+    my_row = (tok0 + ti) * p.q_heads + h * G + int(hi);
+    const int64_t my_off = (tok0 + ti) * p.q_stride + int64_t(h * G + int(hi)) * D;
+#pragma unroll
+    for (int i = 0; i < kRowIter; ++i) {
+      const int64_t off = __shfl_sync(0xffffffffu, my_off, i * kRpi + sub);
+      qv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (warp * 32 + i * kRpi + sub < rows)
+        qv[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off) + c8);
+    }
+  }
 
-  // ---- the largest page exponents, and Q ----
+  // ---- the largest page exponents ----
   {
     int kt = kPageExpMin, vt = kPageExpMin;
     for (int i = tid; i < n_pages; i += kThreads) {
@@ -202,61 +288,17 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     kt = __reduce_max_sync(0xffffffffu, kt);
     vt = __reduce_max_sync(0xffffffffu, vt);
     if (lane == 0) {
-      atomicMax(&bars->k_top, kt);
-      atomicMax(&bars->v_top, vt);
+      bars->k_top[warp] = kt;
+      bars->v_top[warp] = vt;
     }
   }
-  float c = 0.0f;   // factor of a score: z log2 e = S * c
-  int64_t vis = 0;  // keys of the chunk that this thread's row sees
-  if (warp < 8) {
-    const int r = tid;  // row of the CTA, 0 .. 255
-    const bool live = r < rows;
-    const int64_t ri = row0 + r;
-    const uint16_t* src = static_cast<const uint16_t*>(p.q) +
-                          (live ? (s.t_first + ri / G) * p.q_stride + int64_t(h * G + ri % G) * D : 0);
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (live) w = __ldg(reinterpret_cast<const uint4*>(src) + i);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack16(ww[e], p.fp16);
-        amax = max3(amax, fabsf(f.x), fabsf(f.y));
-      }
-    }
-    const int qe = row_exponent(amax);
-    // the sign of the scale goes to Q (c stays positive, so a row's largest S is its largest
-    // score); a zero scale makes Q zero
-    const float f = p.scale == 0.0f ? 0.0f : (p.scale < 0.0f ? -exp2i(-qe) : exp2i(-qe));
-    c = p.scale == 0.0f ? 1.0f : fabsf(p.scale) * kLog2e * exp2i(qe);
-    const uint32_t dst = sbase + uint32_t((r >> 7) * G_::kQBytes + (r & 127) * 128);
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (live) w = __ldg(reinterpret_cast<const uint4*>(src) + i);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        // elements 4j + 0, 2, 1, 3, the order of codes_lo and codes_hi
-        const float2 a = unpack16(ww[e], p.fp16), d = unpack16(ww[e + 1], p.fp16);
-        o[e] = h2(a.x * f, d.x * f);
-        o[e + 1] = h2(a.y * f, d.y * f);
-      }
-      sts128(dst + uint32_t((i >> 3) * 16384) + uint32_t(((i & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-    }
-    int64_t v = s.len;
-    if (p.causal) v = min(v, s.len - s.n + ri / G + 1);
-    vis = live ? v - c0 : 0;
-  }
-  fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const int k_top = bars->k_top, v_top = bars->v_top;
+  int k_top = bars->k_top[min(lane, kWarps - 1)], v_top = bars->v_top[min(lane, kWarps - 1)];
+  k_top = __reduce_max_sync(0xffffffffu, k_top);
+  v_top = __reduce_max_sync(0xffffffffu, v_top);
   int* abort = &bars->abort;
 
   if (warp == kWarpProducer) {
@@ -266,10 +308,11 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     // whose keys begin a TMA box issues the box.
     setmaxnreg_dec<kRegsLow>();
     const int box = ps < kKeys ? ps : kKeys;
+    const int ps_log = 31 - __clz(ps);
     auto page_of = [&](int j) {  // page of this lane's keys in step j, -1: none
       const int key = j * kKeys + lane * 16;
-      if (lane >= 8 || j >= n_steps || key >= keys) return -1;
-      const int pg = __ldg(table + key / ps);
+      if (lane >= kKeys / 16 || j >= n_steps || key >= keys) return -1;
+      const int pg = __ldg(table + (key >> ps_log));
       return pg >= 0 && int64_t(pg) < p.c.num_pages ? pg : -1;
     };
     auto bytes_of = [&](int pg) {
@@ -279,102 +322,99 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     int pg0 = page_of(0), pg1 = page_of(1);
     uint32_t by0 = bytes_of(pg0);
     bool ok = true;
-    int j = 0;
-    for (; ok && j < n_steps; ++j) {
+    int issued = 0;  // units
+    for (int j = 0; ok && j < n_steps; ++j) {
       const int pg2 = page_of(j + 2);
       const uint32_t by1 = bytes_of(pg1);
-      const bool first_of_box = lane < 8 && (lane * 16) % box == 0 && pg0 >= 0;
+      const bool first_of_box = lane < kKeys / 16 && (lane * 16) % box == 0 && pg0 >= 0;
       const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, first_of_box));
       const uint32_t valid = __ballot_sync(0xffffffffu, pg0 >= 0);
-      const int row = int(((int64_t(max(pg0, 0)) * H + h) * ps + (j * kKeys + lane * 16) % ps) * D / 128);
-      // 2^(14 + exponent - top), zero below the range of fp16
-      const int kd = 14 + page_exp(by0 & 0xFFu) - k_top, vd = 14 + page_exp(by0 >> 8) - v_top;
+      const int row = int(((int64_t(max(pg0, 0)) * H + h) * ps + ((j * kKeys + lane * 16) & (ps - 1))) * D / 128);
+      // 2^(6 + exponent - top), zero below the range of fp16
+      const int kd = 6 + page_exp(by0 & 0xFFu) - k_top, vd = 6 + page_exp(by0 >> 8) - v_top;
       const uint32_t kf = h2(exp2i(max(kd, -30)), exp2i(max(kd, -30))), vf = h2(exp2i(max(vd, -30)), exp2i(max(vd, -30)));
 #pragma unroll
       for (int w = 0; ok && w < 2; ++w) {
-        ok = j == 0 || warp_wait(&bars->raw_empty[w], (j - 1) & 1, abort, p.status, kStRawEmpty);
+        const int u = 2 * j + w, slot = u % G_::kRaws;
+        ok = u < G_::kRaws || warp_wait(&bars->raw_empty[slot], (u / G_::kRaws - 1) & 1, abort, p.status, kStRawEmpty);
         if (!ok) break;
-        if (lane < 8) bars->factor[w][lane] = w == 0 ? kf : vf;
-        if (w == 0 && lane == 0) bars->valid[j & 7] = valid;
+        if (lane < kKeys / 16) bars->factor[slot][lane] = w == 0 ? kf : vf;
+        if (w == 0 && lane == 0) bars->valid[j & 15] = valid;
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[w], boxes * uint32_t(box * D));
+        if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[slot], boxes * uint32_t(box * D));
         __syncwarp();
         if (first_of_box)
-          tma_load_2d(sbase + uint32_t((w == 0 ? G_::kOffRawK : G_::kOffRawV) + lane * 16 * D), w == 0 ? &map_k : &map_v, 0,
-                      row, &bars->raw_full[w]);
-        __syncwarp();
+          tma_load_2d(sbase + uint32_t(G_::kOffRaw + slot * G_::kRaw + lane * 16 * D), w == 0 ? &map_k : &map_v, 0, row,
+                      &bars->raw_full[slot]);
+        issued = u + 1;
       }
       pg0 = pg1;
       pg1 = pg2;
       by0 = by1;
     }
-    // the last copies have landed before the CTA may exit (each phase is also waited for by the
-    // converters; after an abort they may have left)
-    if (lane == 0 && j > 0) {
-      for (int w = 0; w < 2; ++w) {
+    // the last copies have landed before the CTA may exit (the converters wait for each of them;
+    // after an abort they may have left)
+    if (!ok && lane == 0) {
+      for (int u = max(issued - G_::kRaws, 0); u < issued; ++u) {
         const uint64_t t0 = globaltimer();
-        while (!ok && !mbar_try_wait(smem_u32(&bars->raw_full[w]), (j - 1) & 1) && globaltimer() - t0 < kTimeoutNs / 4) {
+        while (!mbar_try_wait(smem_u32(&bars->raw_full[u % G_::kRaws]), (u / G_::kRaws) & 1) &&
+               globaltimer() - t0 < kTimeoutNs / 4) {
         }
       }
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ---------------- MMA issuer ----------------
+    // Row tile 0 before row tile 1 in every step: that keeps the two half a step apart. (One issuer
+    // for each let them fall into step, both in their softmax and then both waiting for the tensor
+    // cores: 5400 clocks a step.)
     setmaxnreg_dec<kRegsLow>();
-    const bool leader = elect_one();
     constexpr uint32_t kIdS = (1u << 4) | (uint32_t(kKeys >> 3) << 17) | (uint32_t(128 >> 4) << 24);
     constexpr uint32_t kIdO = (1u << 4) | (1u << 16) /*V is MN-major*/ | (uint32_t(D >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-    auto issue_s = [&](int w, int j) {
-      const uint64_t q = sw128_desc(sbase + uint32_t(w * G_::kQBytes));
-      const uint64_t k = sw128_desc(sbase + uint32_t(G_::kOffK + (j & 1) * G_::kTile));
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t off = uint64_t(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-        mma_ss(tmem + G_::kColS + uint32_t(w * 128), q + off, k + off, kIdS, kk > 0 ? 1u : 0u);
-      }
-      mma_commit(&bars->s_full[w]);
+    auto wait_tile = [&](int u, uint32_t code) {
+      return warp_wait(&bars->t_full[u % G_::kTiles], (u / G_::kTiles) & 1, abort, p.status, code);
     };
-    bool ok = n_steps > 0 && warp_wait(&bars->k_full[0], 0, abort, p.status, kStKFull);
+    auto scores = [&](int w, int j) {
+      const int slot = 2 * j % G_::kTiles;
+      mma_scores<D>(tmem + G_::kColS + uint32_t(w * 128), sw128_desc(sbase + uint32_t(w * G_::kQBytes)),
+                    sw128_desc(sbase + uint32_t(G_::kOffTile + slot * G_::kTile)), kIdS);
+      commit_e(&bars->s_full[w]);
+      if (w == n_tiles - 1) commit_e(&bars->t_empty[slot]);
+    };
+    bool ok = n_steps > 0 && warp_wait(&bars->q_full, 0, abort, p.status, kStQFull) && wait_tile(0, kStKFull);
     if (ok) {
       tc_fence_after();
-      if (leader) {
-        for (int w = 0; w < n_tiles; ++w) issue_s(w, 0);
-        mma_commit(&bars->k_empty[0]);
-      }
-      __syncwarp();
+      for (int w = 0; w < n_tiles; ++w) scores(w, 0);
     }
+    // P V of step j (each half of the keys as soon as its P is there), then the row tile's next
+    // scores, which overwrite P
     for (int j = 0; ok && j < n_steps; ++j) {
-      const int st = j & 1;
-      for (int w = 0; w < n_tiles; ++w) {
-        ok = warp_wait(&bars->p_full[w], j & 1, abort, p.status, kStPFull);
-        if (ok && w == 0) ok = warp_wait(&bars->v_full[st], (j >> 1) & 1, abort, p.status, kStVFull);
+      const int slot = (2 * j + 1) % G_::kTiles;
+      const uint64_t v = desc_lbo(sbase + uint32_t(G_::kOffTile + slot * G_::kTile), kKeys * 128);
+      ok = wait_tile(2 * j + 1, kStVFull);
+      for (int w = 0; ok && w < n_tiles; ++w) {
+        const uint32_t t_o = tmem + G_::kColO + uint32_t(w * D), t_p = tmem + G_::kColS + uint32_t(w * 128);
+        ok = warp_wait(&bars->p_full[w][0], j & 1, abort, p.status, kStPFull);
         if (!ok) break;
         tc_fence_after();
-        if (leader) {
-          const uint64_t v = desc_lbo(sbase + uint32_t(G_::kOffV + st * G_::kTile), 16384);
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(tmem + G_::kColO + uint32_t(w * D), tmem + G_::kColS + uint32_t(w * 128 + kk * 8),
-                   v + uint64_t((kk * 2048) >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
-          if (w == n_tiles - 1) mma_commit(&bars->v_empty[st]);
-          if (j == n_steps - 1) mma_commit(&bars->o_full[w]);
-        }
-        __syncwarp();
+        mma_values(t_o, t_p, v, kIdO, j > 0 ? 1u : 0u);
+        ok = warp_wait(&bars->p_full[w][1], j & 1, abort, p.status, kStPFull);
+        if (!ok) break;
+        tc_fence_after();
+        mma_values(t_o, t_p + 32, v + uint64_t((64 * 128) >> 4), kIdO, 1u);
+        if (w == n_tiles - 1) commit_e(&bars->t_empty[slot]);
         if (j + 1 < n_steps) {
-          if (w == 0) ok = warp_wait(&bars->k_full[st ^ 1], ((j + 1) >> 1) & 1, abort, p.status, kStKFull);
+          if (w == 0) ok = wait_tile(2 * j + 2, kStKFull);
           if (!ok) break;
           tc_fence_after();
-          if (leader) {
-            issue_s(w, j + 1);
-            if (w == n_tiles - 1) mma_commit(&bars->k_empty[st ^ 1]);
-          }
-          __syncwarp();
+          scores(w, j + 1);
+        } else {
+          commit_e(&bars->o_full[w]);
         }
       }
     }
     // every MMA issued here has completed before TMEM is released
-    if (leader) mma_commit(&bars->mma_done);
-    __syncwarp();
+    commit_e(&bars->mma_done);
     if (lane == 0) {
       const uint64_t t0 = globaltimer();
       while (!mbar_try_wait(smem_u32(&bars->mma_done), 0)) {
@@ -393,40 +433,63 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const int cw = warp - kWarpConv0;
     constexpr int kChunks = D / 16;  // 16-code chunks of a key
     constexpr int kIter = kKeys * kChunks / 128;
+    constexpr int kBatch = kIter < 4 ? kIter : 4;
+    const int key0 = cw * 8 + (lane & 7), ch0 = lane >> 3;
     bool ok = true;
-    for (int j = 0; ok && j < n_steps; ++j) {
-      const int st = j & 1;
-#pragma unroll 1
-      for (int w = 0; ok && w < 2; ++w) {
-        ok = warp_wait(&bars->raw_full[w], j & 1, abort, p.status, kStRawFull);
-        if (ok && j >= 2)
-          ok = warp_wait(w == 0 ? &bars->k_empty[st] : &bars->v_empty[st], ((j >> 1) - 1) & 1, abort, p.status,
-                         w == 0 ? kStKEmpty : kStVEmpty);
-        if (!ok) break;
-        const uint32_t raw = sbase + uint32_t(w == 0 ? G_::kOffRawK : G_::kOffRawV);
-        const uint32_t dst = sbase + uint32_t((w == 0 ? G_::kOffK : G_::kOffV) + st * G_::kTile);
+    for (int u = 0; ok && u < 2 * n_steps; ++u) {
+      const int slot = u % G_::kRaws, tile_slot = u % G_::kTiles;
+      ok = warp_wait(&bars->raw_full[slot], (u / G_::kRaws) & 1, abort, p.status, kStRawFull);
+      if (ok && u >= G_::kTiles)
+        ok = warp_wait(&bars->t_empty[tile_slot], (u / G_::kTiles - 1) & 1, abort, p.status, kStTEmpty);
+      if (!ok) break;
+      const uint32_t raw = sbase + uint32_t(G_::kOffRaw + slot * G_::kRaw);
+      const uint32_t dst = sbase + uint32_t(G_::kOffTile + tile_slot * G_::kTile);
+      const uint32_t* factor = bars->factor[slot];
+      // iteration it of a warp: eight keys (it % 4) * 32 + key0, chunks (it / 4) * 4 + ch0
+      auto convert = [&](auto fast) {
 #pragma unroll
-        for (int it = 0; it < kIter; ++it) {
-          // groups of 8 keys x 4 chunks per warp and iteration
-          const int unit = it * 4 + cw;
-          const int key = (unit % 16) * 8 + (lane & 7);
-          const int ch = (unit / 16) * 4 + (lane >> 3);
-          const uint32_t o = uint32_t(key * D + ch * 16);
-          const uint4 v = lds128(raw + (o ^ (((o >> 7) & 7u) << 4)));
-          const uint32_t f = bars->factor[w][key >> 4];
-          const uint32_t at = dst + uint32_t((ch >> 2) * 16384 + key * 128);
-          const uint32_t c2 = uint32_t((ch & 3) * 2), k7 = uint32_t(key & 7);
-          sts128(at + ((c2 ^ k7) << 4), hmul2(codes_lo(v.x), f), hmul2(codes_hi(v.x), f), hmul2(codes_lo(v.y), f),
-                 hmul2(codes_hi(v.y), f));
-          sts128(at + (((c2 + 1) ^ k7) << 4), hmul2(codes_lo(v.z), f), hmul2(codes_hi(v.z), f), hmul2(codes_lo(v.w), f),
-                 hmul2(codes_hi(v.w), f));
+        for (int b = 0; b < kIter; b += kBatch) {
+          uint4 v[kBatch];
+          uint32_t f[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int key = ((b + i) & 3) * 32 + key0, ch = ((b + i) >> 2) * 4 + ch0;
+            const uint32_t o = uint32_t(key * D + ch * 16);
+            v[i] = lds128(raw + (o ^ (((o >> 7) & 7u) << 4)));
+            f[i] = factor[key >> 4];
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int key = ((b + i) & 3) * 32 + key0, ch = ((b + i) >> 2) * 4 + ch0;
+            const uint32_t at = dst + uint32_t((ch >> 2) * (kKeys * 128) + key * 128);
+            const uint32_t c2 = uint32_t((ch & 3) * 2), k7 = uint32_t(key & 7);
+            uint32_t y[8];
+            if constexpr (decltype(fast)::value) {
+              cvt4(v[i].x, y);
+              cvt4(v[i].y, y + 2);
+              cvt4(v[i].z, y + 4);
+              cvt4(v[i].w, y + 6);
+            } else {
+              bits4(v[i].x, y);
+              bits4(v[i].y, y + 2);
+              bits4(v[i].z, y + 4);
+              bits4(v[i].w, y + 6);
+            }
+            sts128(at + ((c2 ^ k7) << 4), hmul2(y[0], f[i]), hmul2(y[1], f[i]), hmul2(y[2], f[i]), hmul2(y[3], f[i]));
+            sts128(at + (((c2 + 1) ^ k7) << 4), hmul2(y[4], f[i]), hmul2(y[5], f[i]), hmul2(y[6], f[i]), hmul2(y[7], f[i]));
+          }
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->raw_empty[w]);
-          mbar_arrive(w == 0 ? &bars->k_full[st] : &bars->v_full[st]);
-        }
+      };
+      // a step whose every key is there takes the hardware conversion (half the instructions);
+      // its codes are numbers, while stale bytes may be E4M3's NaN pattern
+      const int j = u >> 1;
+      if (bars->valid[j & 15] == kAllThere && (j + 1) * kKeys <= keys) convert(std::true_type());
+      else convert(std::false_type());
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars->raw_empty[slot]);
+        mbar_arrive(&bars->t_full[tile_slot]);
       }
     }
   } else if (warp < 8) {
@@ -435,7 +498,38 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const int w = warp >> 2;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + G_::kColS + uint32_t(w * 128), t_o = t_lane + G_::kColO + uint32_t(w * D);
-    if (p.scale != 0.0f) c = fmaxf(c * exp2i(k_top + 8 - 14), 1e-37f);  // positive: -inf * c is -inf
+    float c = 1.0f;   // factor of a score: z log2 e = S * c
+    int64_t vis = 0;  // keys of the chunk that this thread's row sees
+    if (w < n_tiles) {
+      // the sign of the scale goes to Q (c stays positive, so a row's largest S is its largest
+      // score); a zero scale makes Q zero
+      const float sign = p.scale == 0.0f ? 0.0f : (p.scale < 0.0f ? -1.0f : 1.0f);
+#pragma unroll
+      for (int i = 0; i < kRowIter; ++i) {
+        const int r = warp * 32 + i * kRpi + sub;
+        const float2 x0 = unpack16(qv[i].x, kF16), x1 = unpack16(qv[i].y, kF16), x2 = unpack16(qv[i].z, kF16),
+                     x3 = unpack16(qv[i].w, kF16);
+        float amax = max3(fmaxf(fabsf(x3.x), fabsf(x3.y)), max3(fabsf(x0.x), fabsf(x0.y), fabsf(x1.x)),
+                          max3(fabsf(x1.y), fabsf(x2.x), fabsf(x2.y)));
+#pragma unroll
+        for (int o = kLpr / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int qe = row_exponent(amax);
+        const float f = sign * exp2i(-qe);
+        const uint32_t dst = sbase + uint32_t((r >> 7) * G_::kQBytes + (c8 >> 3) * 16384 + (r & 127) * 128);
+        sts128(dst + uint32_t(((c8 & 7) ^ (r & 7)) << 4), h2(x0.x * f, x0.y * f), h2(x1.x * f, x1.y * f),
+               h2(x2.x * f, x2.y * f), h2(x3.x * f, x3.y * f));
+        if (c8 == 0) bars->q_exp[r] = int8_t(qe);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_full);
+      const unsigned ti = (rem0 + unsigned(tid)) / Gu;
+      if (p.scale != 0.0f) c = fabsf(p.scale) * kLog2e * exp2i(bars->q_exp[tid]);
+      int64_t v = s.len;
+      if (p.causal) v = min(v, s.len - s.n + i0 + int64_t(ti) + 1);
+      vis = tid < rows ? v - c0 : 0;
+    }
+    if (p.scale != 0.0f) c = fmaxf(c * exp2i(k_top - 6), 1e-37f);  // positive: -inf * c is -inf
     float m = -INFINITY;  // the row's maximum that the exponents are taken against (of S)
     float2 l2 = make_float2(0.0f, 0.0f);
     bool ok = true;
@@ -444,46 +538,53 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         ok = warp_wait(&bars->s_full[w], j & 1, abort, p.status, kStSFull);
         if (!ok) break;
         tc_fence_after();
-        float x[kKeys];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(t_s + uint32_t(i * 32), reinterpret_cast<uint32_t*>(x) + i * 32);
-        tmem_wait_ld();
         const int left = int(min(vis - int64_t(j) * kKeys, int64_t(kKeys)));  // keys of the step that the row sees
-        const uint32_t valid = bars->valid[j & 7];
-        if (__any_sync(0xffffffffu, left < kKeys) || valid != 0xFFu) {
+        const uint32_t valid = bars->valid[j & 15];
+        const bool masked = __any_sync(0xffffffffu, left < kKeys) || valid != kAllThere;
+        float x[kKeys];
+        auto load = [&]() {
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-            if (i >= left || ((valid >> (i / 16)) & 1u) == 0u) x[i] = -INFINITY;
-        }
+          for (int i = 0; i < kKeys / 32; ++i) tmem_ld32(t_s + uint32_t(i * 32), reinterpret_cast<uint32_t*>(x) + i * 32);
+          tmem_wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+              if (i >= left || ((valid >> (i / 16)) & 1u) == 0u) x[i] = -INFINITY;
+          }
+        };
+        load();
         float a0 = x[0], a1 = x[1], a2 = x[2], a3 = x[3];
 #pragma unroll
-        for (int i = 4; i < kKeys; i += 8) {
+        for (int i = 4; i < kKeys - 4; i += 8) {
           a0 = max3(a0, x[i], x[i + 1]);
           a1 = max3(a1, x[i + 2], x[i + 3]);
-          if (i + 4 < kKeys) {
-            a2 = max3(a2, x[i + 4], x[i + 5]);
-            a3 = max3(a3, x[i + 6], x[i + 7]);
-          }
+          a2 = max3(a2, x[i + 4], x[i + 5]);
+          a3 = max3(a3, x[i + 6], x[i + 7]);
         }
-        const float top = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
-        // raise the maximum where the row is beyond it by 2^8 (or had none)
-        const bool raise = top > m && !((top - m) * c <= 8.0f);
+        a0 = max3(a0, x[kKeys - 4], x[kKeys - 3]);
+        a1 = max3(a1, x[kKeys - 2], x[kKeys - 1]);
+        const float top = max3(fmaxf(a0, a1), a2, a3);
+        // raise the maximum where the row is beyond it by 2^15 (or had none)
+        const bool raise = top > m && !((top - m) * c <= 15.0f);
         if (__any_sync(0xffffffffu, raise)) {
           const float alpha = raise ? (m == -INFINITY ? 0.0f : fast_exp2((m - top) * c)) : 1.0f;
           if (raise) m = top;
           l2.x *= alpha;
           l2.y *= alpha;
           if (j > 0) {
-            // S(j) was issued after P V (j - 1) and has completed, so O is at rest
+            // S of this step was issued after P V of the last and is complete, so O is at rest. The
+            // scores are read again after it: their registers serve here.
 #pragma unroll
-            for (int i = 0; i < D; i += 16) {
-              uint32_t o[16];
-              tmem_ld16(t_o + uint32_t(i), o);
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + uint32_t(i), o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
               tmem_st16(t_o + uint32_t(i), o);
+              tmem_st16(t_o + uint32_t(i + 16), o + 16);
             }
+            load();
           }
         }
         const float mu = m == -INFINITY ? 0.0f : m;
@@ -504,52 +605,73 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             pk[e / 2 + 1] = h2(v.x, v.y);
           }
           tmem_st16(t_s + uint32_t(i / 2), pk);
+          if (i % 64 == 32) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[w][i / 64]);
+          }
         }
         l2 = __fadd2_rn(l2, __fadd2_rn(sum0, sum1));
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[w]);
       }
       if (ok && n_steps > 0) ok = warp_wait(&bars->o_full[w], 0, abort, p.status, kStOFull);
       if (ok) {
         tc_fence_after();
         const int r = tid;
         const bool live = r < rows;
-        const int64_t ri = row0 + r;
-        const int64_t row = (s.t_first + ri / G) * p.q_heads + h * G + ri % G;
+        const int64_t row = my_row;
         const float L = l2.x + l2.y;
         const float mz = m == -INFINITY ? -INFINITY : m * c;
-        const float unit = exp2i(v_top + 8 - 14);
+        const float unit = exp2i(v_top - 6);
         const float inv = whole ? (L > 0.0f ? unit / L : 0.0f) : unit;
+        if (whole) {
+          // through shared memory (this warp's rows of Q, which every MMA is done with), so that a
+          // row's 16-byte pieces leave side by side
+          const uint32_t mine = sbase + uint32_t(w * G_::kQBytes + (warp & 3) * 32 * D * 2);
+          constexpr int kPieces = kLpr;
 #pragma unroll
-        for (int i = 0; i < D; i += 16) {
-          uint32_t o[16];
-          if (n_steps > 0) {
-            tmem_ld16(t_o + uint32_t(i), o);
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            if (n_steps > 0) {
+              tmem_ld32(t_o + uint32_t(i), o);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                y[q] = pack16(__uint_as_float(o[e + 2 * q]) * inv, __uint_as_float(o[e + 2 * q + 1]) * inv, kF16);
+              const int piece = (i + e) / 8;
+              sts128(mine + uint32_t(lane * D * 2) + uint32_t((piece ^ (lane & 7)) << 4), y[0], y[1], y[2], y[3]);
+            }
+          }
+          __syncwarp();
+          const int piece = lane % kPieces;
+#pragma unroll
+          for (int i = 0; i < 32 / kRpi; ++i) {
+            const int rr = i * kRpi + lane / kPieces;
+            const uint4 y = lds128(mine + uint32_t(rr * D * 2) + uint32_t((piece ^ (rr & 7)) << 4));
+            const int64_t to = __shfl_sync(0xffffffffu, my_row, rr);
+            if (warp * 32 + rr < rows)
+              *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to * D) + piece) = y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + uint32_t(i), o);
             tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0u;
-          }
-          float y[16];
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {  // columns 0, 2, 1, 3 of every four
-            y[e] = __uint_as_float(o[e]) * inv;
-            y[e + 1] = __uint_as_float(o[e + 2]) * inv;
-            y[e + 2] = __uint_as_float(o[e + 1]) * inv;
-            y[e + 3] = __uint_as_float(o[e + 3]) * inv;
-          }
-          if (live && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + i);
-            dst[0] = make_uint4(pack16(y[0], y[1], p.fp16), pack16(y[2], y[3], p.fp16), pack16(y[4], y[5], p.fp16),
-                                pack16(y[6], y[7], p.fp16));
-            dst[1] = make_uint4(pack16(y[8], y[9], p.fp16), pack16(y[10], y[11], p.fp16), pack16(y[12], y[13], p.fp16),
-                                pack16(y[14], y[15], p.fp16));
-          } else if (live) {
             float4* dst = reinterpret_cast<float4*>(p.ws + (row * p.ws_splits + split) * (D + 4) + i);
+            if (live) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) dst[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+              for (int e = 0; e < 32; e += 4)
+                dst[e / 4] = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                         __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            }
           }
         }
         if (live && whole) {
@@ -573,7 +695,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   }
 }
 
-template <int D>
+template <int D, bool kF16>
 cudaError_t launch_tc(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_t stream) {
   const uint64_t rows128 = uint64_t(p.c.num_pages) * p.c.kv_heads * p.c.page_size * D / 128;
   const int box = (p.c.page_size < kKeys ? p.c.page_size : kKeys) * D / 128;
@@ -581,12 +703,12 @@ cudaError_t launch_tc(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_
   if (!encode_bytes_2d(&map_k, p.c.k, rows128, 128, 128, uint32_t(box)) ||
       !encode_bytes_2d(&map_v, p.c.v, rows128, 128, 128, uint32_t(box)))
     return cudaErrorInvalidValue;
-  auto kern = kv_attn_tc_kernel<D>;
+  auto kern = kv_attn_tc_kernel<D, kF16>;
   // setmaxnreg.inc draws on what the block was launched with
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != 128) return cudaErrorInvalidKernelImage;
+  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t grid = int64_t(plan.tc_row_tiles) * p.c.kv_heads * plan.tc_splits * p.b.num_seqs;
@@ -598,7 +720,9 @@ cudaError_t launch_tc(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_
 }  // namespace
 
 cudaError_t launch_kv_attn_tc(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_t stream) {
-  return p.c.head_dim == 128 ? launch_tc<128>(p, plan, stream) : launch_tc<64>(p, plan, stream);
+  if (p.c.head_dim == 128)
+    return p.fp16 ? launch_tc<128, true>(p, plan, stream) : launch_tc<128, false>(p, plan, stream);
+  return p.fp16 ? launch_tc<64, true>(p, plan, stream) : launch_tc<64, false>(p, plan, stream);
 }
 
 }  // namespace fq

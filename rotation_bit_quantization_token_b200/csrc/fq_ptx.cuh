@@ -76,16 +76,19 @@ __device__ __forceinline__ void named_bar(int id, int count) {
 }
 
 // Bounded wait on a phase; on expiry (or once another role has given up) it sets *abort and
-// a status bit and returns false.
+// a status bit and returns false. The clock is read once in 64 tries: reading it takes longer
+// than most waits here last, and a phase that completes meanwhile would be seen late.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, int* abort, uint32_t* status,
                                              uint32_t code) {
   const uint32_t b = smem_u32(bar);
-  if (mbar_try_wait(b, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (;;) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(b, parity)) return true;
+    if ((i & 63u) != 0u) continue;
     if (*reinterpret_cast<volatile int*>(abort)) return false;
-    if (globaltimer() - t0 > kTimeoutNs) {
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kTimeoutNs) {
       *reinterpret_cast<volatile int*>(abort) = 1;
       if (status != nullptr) atomicOr(status, code);
       return false;
