@@ -40,6 +40,7 @@ struct KvAttnParams {
   float scale;
   int chunk;         // keys of one split
   int splits;        // splits of the longest sequence
+  int tile_rows;     // rows of a CTA (8 or 16)
   int64_t tc_rows;   // sequences with more rows (new tokens * group) take the tensor-core kernel
   int tc_chunk, tc_splits;
   int ws_splits;     // slots per row of the workspace: max(splits, tc_splits)
@@ -47,7 +48,7 @@ struct KvAttnParams {
 
 // How fq_kv_attention divides its work; the workspace follows from it.
 struct KvAttnPlan {
-  int chunk, splits, row_tiles;             // mma.sync kernel: 16 rows and one chunk per CTA; 0 row tiles: not launched
+  int chunk, splits, tile_rows, row_tiles;  // mma.sync kernel: tile_rows rows and one chunk per CTA; 0 tiles: not launched
   int tc_chunk, tc_splits, tc_row_tiles;    // tensor-core kernel: 256 rows and one chunk per CTA; 0: not launched
   int64_t tc_rows;
   int64_t ws_bytes;

@@ -129,7 +129,7 @@ fq_status fq_kv_attention(const fq_kv_cache* cache, const fq_kv_batch* batch, in
   p.c = *cache; p.b = *batch; p.q = q; p.out = out; p.lse = lse; p.ws = static_cast<float*>(workspace);
   p.status = status; p.T = T; p.q_stride = q_stride; p.max_seq_len = max_seq_len; p.q_heads = q_heads;
   p.max_q_len = max_q_len; p.causal = causal; p.fp16 = dtype == FQ_FP16; p.scale = float(scale);
-  p.chunk = plan.chunk; p.splits = plan.splits; p.tc_rows = plan.tc_rows;
+  p.chunk = plan.chunk; p.splits = plan.splits; p.tile_rows = plan.tile_rows; p.tc_rows = plan.tc_rows;
   p.tc_chunk = plan.tc_chunk; p.tc_splits = plan.tc_splits;
   p.ws_splits = plan.splits > plan.tc_splits ? plan.splits : plan.tc_splits;
   const cudaError_t e = fq::launch_kv_attn(p, plan, reinterpret_cast<cudaStream_t>(stream));

@@ -1,26 +1,32 @@
-// Attention over the 8-bit paged cache: softmax(scale q k^T) v, for any number of new tokens.
+// Attention over the 8-bit paged cache for sequences with few rows: decode steps.
 //
-// Rows are (new token, query head) pairs that share one key / value head, packed 16 at a time
-// (row r of a sequence: token r / G, head r % G of the group, G = q_heads / kv_heads), so a
-// decode step reads each cached byte once for the whole group. With few rows the kernel is
-// bound by reading the cache: 2 D bytes a token and head.
+// Rows are (new token, query head) pairs that share one key / value head (row r of a sequence: token
+// r / G, head r % G of the group, G = q_heads / kv_heads), 8 or 16 of them per CTA, so a decode step
+// reads each cached byte once for the whole group. The kernel is bound by reading the cache: 2 D
+// bytes a token and head.
 //
-// One CTA takes 16 rows and one chunk of keys; its four warps take tiles of 32 keys in turn,
+// One CTA takes its rows and one chunk of keys; its four warps take tiles of 4096 / D keys in turn,
 // each through a ring of its own (TMA boxes of 128-byte rows, swizzled; no barrier between the
-// warps), with a running maximum, sum and output of its own; they are joined through shared
-// memory at the end. A sequence longer than one chunk is joined by a second kernel from partial
-// results in the workspace.
+// warps), with a running maximum, sum and output of its own; they are joined through shared memory
+// at the end. A sequence longer than one chunk is joined by a second kernel from partial results in
+// the workspace.
 //
-// Numbers. A code is converted to fp16 with integer operations (E4M3 bits moved into the fp16
-// fields give code * 2^-8, subnormals included; every bit pattern gives a finite number, so
-// stale bytes behind the last token cannot put a NaN into the sum). A row of q is scaled by the
-// power of two that brings its largest magnitude into [2^14, 2^15) and converted to fp16: exact
-// but for elements 2^-29 below the largest. The products are then exact in the fp32 sums of
-// mma.sync, and the powers of two (q row, page of k, 2^8) are applied to the score in float32.
-// Probabilities are rounded to fp16 (2^-11) for the second product. The output accumulates in
-// units of the page's own scale of v and moves to the next page's unit by a power of two, so
-// that no page's scale has to fit beside another's in fp16: exponents lie in [-40, 40], so a
-// unit changes by at most 2^80 and float32 holds all of it.
+// Products are mma.sync with the keys (then the output columns) on the M side and the rows on N: with
+// 8 rows nothing is padded, and a thread holds a quarter of the output registers of the other
+// orientation. S^T = K Q^T: a thread's words of K are codes of neighbouring d, which two conversions
+// turn into one A fragment (the sum over d may run in any order, so q is held in the order that the
+// words give). O^T += V^T P^T: P^T's fragments are those of S^T, transposed in registers (movmatrix);
+// V^T's put two keys side by side, one byte permute for two codes.
+//
+// Numbers. A code becomes fp16 by the hardware conversion; keys behind the last token (or on a
+// missing page) are zeroed in shared memory first, since stale bytes may be E4M3's NaN pattern. A row
+// of q is scaled by the power of two that brings its largest magnitude into [2^14, 2^15) and
+// converted to fp16: exact but for elements 2^-29 below the largest. The products are then exact in
+// the fp32 sums of mma.sync, and the powers of two (q row, page of k) are applied to the score in
+// float32. Probabilities are rounded to fp16 (2^-11) for the second product. The output accumulates
+// in units of the page's own scale of v and moves to the next page's unit by a power of two, so that
+// no page's scale has to fit beside another's in fp16: exponents lie in [-40, 40], so a unit changes
+// by at most 2^80 and float32 holds all of it.
 #include <cstdint>
 
 #include "fq_kv_common.cuh"
@@ -32,24 +38,26 @@ using namespace ptx;
 using namespace kv;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTileKeys = 32;   // keys of one warp's step
-constexpr int kRowsTile = 16;   // rows of a CTA
 constexpr int kMaxChunk = 8192; // keys of a chunk (its page numbers sit in shared memory)
+
 enum : uint32_t { kStFull = 1u << 0 };
 
-template <int D>
+template <int D, int NT>
 struct Geo {
-  static constexpr int kTileBytes = kTileKeys * D;          // codes of K (or V) of a tile
+  static constexpr int kRows = 8 * NT;                      // rows of a CTA
+  static constexpr int kTileKeys = 4096 / D;                // keys of one warp's step
+  static constexpr int kTileBytes = 4096;                   // codes of K (or V) of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = NT == 1 ? 2 : 3;
+  static constexpr int kMinBlocks = NT == 1 ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kOStride = D + 4;                    // floats per row of a warp's output
-  static_assert(kWarps * kRowsTile * kOStride * 4 <= kRing, "outputs fit the ring");
+  static_assert(kWarps * kRows * kOStride * 4 <= kRing, "outputs fit the ring");
 };
 
 struct Shared {
-  uint64_t full[kWarps][8];
-  float m[kWarps][kRowsTile], l[kWarps][kRowsTile];
+  uint64_t full[kWarps][4];
+  float m[kWarps][16], l[kWarps][16];
   int abort;
 };
 
@@ -77,27 +85,43 @@ __device__ __forceinline__ uint32_t swz(int key, int d) {
   return o ^ (((o >> 7) & 7u) << 4);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+// Two E4M3 codes (the low and the high half of w) as two fp16 numbers each.
+__device__ __forceinline__ void cvt4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+// Transposes the warp's 8 x 8 matrix of 16-bit elements (lane 4r + c holds row r, columns 2c, 2c + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Geo<D, NT>::kMinBlocks)
 kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                const KvAttnParams p, const int row_tiles) {
-  using G_ = Geo<D>;
-  constexpr int kS = D / 16;      // k steps of q k^T
-  constexpr int kN = D / 8;       // 8-column blocks of the output
+  using G_ = Geo<D, NT>;
+  constexpr int kTK = G_::kTileKeys, kRowsTile = G_::kRows;
+  constexpr int kS = D / 16;      // k steps of q k^T, 16-column blocks of the output
+  constexpr int kMT = kTK / 16;   // blocks of 16 keys of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Shared* sh = reinterpret_cast<Shared*>(smem + G_::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int ps = p.c.page_size, H = p.c.kv_heads, G = p.q_heads / H;
+  const int H = p.c.kv_heads, G = p.q_heads / H;
+  const int ps_log = 31 - __clz(p.c.page_size), ps = 1 << ps_log;
 
-  int64_t idx = blockIdx.x;
-  const int tile = int(idx % row_tiles);
-  idx /= row_tiles;
-  const int h = int(idx % H);
-  idx /= H;
-  const int split = int(idx % p.splits);
-  const int b = int(idx / p.splits);
+  unsigned idx = blockIdx.x;
+  const int tile = int(idx % unsigned(row_tiles));
+  idx /= unsigned(row_tiles);
+  const int h = int(idx % unsigned(H));
+  idx /= unsigned(H);
+  const int split = int(idx % unsigned(p.splits));
+  const int b = int(idx / unsigned(p.splits));
 
   const Rows s = sequence_rows(p, b, int64_t(tile) * kRowsTile, kRowsTile, G);
   if (tid == 0 && split == 0 && h == 0 && tile == 0 && p.status != nullptr && (!s.ok || s.n > p.max_q_len))
@@ -113,11 +137,11 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   // ---- page numbers of the chunk, barriers ----
   // scales beside them: (k exponent, v exponent) as bytes; a page outside the cache is -1
   int* s_page = reinterpret_cast<int*>(sh + 1);
-  uint16_t* s_scale = reinterpret_cast<uint16_t*>(s_page + (p.chunk + ps - 1) / ps);
-  const int n_pages = (keys + ps - 1) / ps;
+  uint16_t* s_scale = reinterpret_cast<uint16_t*>(s_page + (p.chunk >> ps_log) + 1);
+  const int n_pages = (keys + ps - 1) >> ps_log;
   if (tid < kWarps * G_::kStages) mbar_init(&sh->full[tid / G_::kStages][tid % G_::kStages], 1);
   if (tid == 0) sh->abort = 0;
-  const int* table = p.b.page_table + int64_t(b) * p.b.table_width + c0 / ps;
+  const int* table = p.b.page_table + int64_t(b) * p.b.table_width + (c0 >> ps_log);
   for (int i = tid; i < n_pages; i += kThreads) {
     int pg = __ldg(table + i);
     if (pg < 0 || int64_t(pg) >= p.c.num_pages) {
@@ -132,49 +156,50 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   }
   __syncthreads();
 
-  const int n_tiles = (keys + kTileKeys - 1) / kTileKeys;
+  const int n_tiles = (keys + kTK - 1) / kTK;
   const uint32_t ring = smem_u32(smem) + uint32_t(warp * G_::kStages * G_::kStageBytes);
-  const int box = ps < kTileKeys ? ps : kTileKeys;  // keys of one TMA box
-  // loads tile w of the chunk into a stage (one lane); boxes that start behind the last key, or
-  // whose page is missing, are left out: their keys are masked
+  const int box_log = min(ps_log, kTK == 32 ? 5 : 6);  // keys of one TMA box
+  // Loads tile w of the chunk into a stage: lane 2i takes box i of K, lane 2i + 1 box i of V. Boxes
+  // that start behind the last key, or whose page is missing, are left out.
   auto issue = [&](int w, int stage) {
     uint64_t* bar = &sh->full[warp][stage];
-    const uint32_t dst = ring + uint32_t(stage * G_::kStageBytes);
-    uint32_t bytes = 0;
-    for (int k = 0; k < kTileKeys && w * kTileKeys + k < keys; k += box)
-      if (s_page[(w * kTileKeys + k) / ps] >= 0) bytes += uint32_t(2 * box * D);
-    mbar_arrive_expect_tx(bar, bytes);
-    for (int k = 0; k < kTileKeys && w * kTileKeys + k < keys; k += box) {
-      const int at = w * kTileKeys + k;
-      const int pg = s_page[at / ps];
-      if (pg < 0) continue;
-      const int row = int(((int64_t(pg) * H + h) * ps + at % ps) * D / 128);
-      tma_load_2d(dst + uint32_t(k * D), &map_k, 0, row, bar);
-      tma_load_2d(dst + uint32_t(G_::kTileBytes + k * D), &map_v, 0, row, bar);
+    const int at = w * kTK + ((lane >> 1) << box_log);
+    int pg = -1;
+    if (((lane >> 1) << box_log) < kTK && at < keys) pg = s_page[at >> ps_log];
+    const uint32_t n = uint32_t(__popc(__ballot_sync(0xffffffffu, pg >= 0)));
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * uint32_t(D << box_log));
+    __syncwarp();
+    if (pg >= 0) {
+      const int row = int((((int64_t(pg) * H + h) << ps_log) + (at & (ps - 1))) * D / 128);
+      const uint32_t dst = ring + uint32_t(stage * G_::kStageBytes + (lane & 1) * G_::kTileBytes + ((lane >> 1) << box_log) * D);
+      tma_load_2d(dst, (lane & 1) ? &map_v : &map_k, 0, row, bar);
     }
   };
-  if (lane == 0)
-    for (int st = 0; st < G_::kStages; ++st)
-      if (warp + st * kWarps < n_tiles) issue(warp + st * kWarps, st);
+#pragma unroll
+  for (int st = 0; st < G_::kStages; ++st)
+    if (warp + st * kWarps < n_tiles) issue(warp + st * kWarps, st);
 
+  bool missing = false;  // a page of the chunk is not there
   for (int i = tid; i < n_pages; i += kThreads) {
     const int pg = s_page[i];
     int ke = 0, ve = 0;
     if (pg >= 0) {
       ke = page_exp(__ldg(p.c.k_scale + int64_t(pg) * H + h));
       ve = page_exp(__ldg(p.c.v_scale + int64_t(pg) * H + h));
+    } else {
+      missing = true;
     }
     s_scale[i] = uint16_t((ke + 127) | ((ve + 127) << 8));
   }
 
-  // ---- q: this thread's elements of rows g and g + 8, t4 * D/4 .. + D/4 ----
-  uint32_t qf[kS][4];
-  float rowf[2];
-  int64_t vis[2];  // keys of the chunk that the row sees
+  // ---- q: this thread's elements t4 * D/4 .. + D/4 of row g (and g + 8) ----
+  uint32_t qf[NT][kS][2];
+  float rowf[NT][2];  // score factor of rows 2 t4, 2 t4 + 1 (+ 8)
+  int vis[NT][2];     // keys of the chunk that they see
 #pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
-    const int r = row0 + g + 8 * hh;
-    const bool live = g + 8 * hh < rows;
+  for (int n = 0; n < NT; ++n) {
+    const int r = row0 + g + 8 * n;
+    const bool live = g + 8 * n < rows;
     float x[D / 4];
     float amax = 0.0f;
     const int64_t base = live ? (s.t_first + r / G) * p.q_stride + int64_t(h * G + r % G) * D + t4 * (D / 4) : 0;
@@ -197,117 +222,168 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     const float f = exp2i(-qe);
 #pragma unroll
     for (int st = 0; st < kS; ++st) {
-      qf[st][hh] = h2(x[4 * st] * f, x[4 * st + 2] * f);          // k pairs as codes_lo gives them
-      qf[st][2 + hh] = h2(x[4 * st + 1] * f, x[4 * st + 3] * f);  // and codes_hi
+      qf[n][st][0] = h2(x[4 * st] * f, x[4 * st + 1] * f);
+      qf[n][st][1] = h2(x[4 * st + 2] * f, x[4 * st + 3] * f);
     }
-    rowf[hh] = p.scale * kLog2e * exp2i(qe);
     int64_t v = s.len;
     if (p.causal) v = min(v, s.len - s.n + int64_t(r / G) + 1);
-    vis[hh] = live ? v - c0 : 0;
+    const int see = live ? int(max(min(v - c0, int64_t(keys)), int64_t(0))) : 0;
+    const float rf = p.scale * kLog2e * exp2i(qe);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // row 2 t4 + e belongs to the lanes of g = 2 t4 + e
+      rowf[n][e] = __shfl_sync(0xffffffffu, rf, (2 * t4 + e) * 4);
+      vis[n][e] = __shfl_sync(0xffffffffu, see, (2 * t4 + e) * 4);
+    }
   }
-  __syncthreads();  // scales
+  int all_see = keys;  // keys that every row sees
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (8 * n + 2 * t4 + e < rows) all_see = min(all_see, vis[n][e]);
+  all_see = __reduce_min_sync(0xffffffffu, all_see);
+  missing = __syncthreads_or(missing);  // and the scales are there
 
-  float o[kN][4];
+  float o[kS][NT][4];
 #pragma unroll
-  for (int j = 0; j < kN; ++j)
+  for (int j = 0; j < kS; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][n][e] = 0.0f;
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[n][e] = -INFINITY;
+      l[n][e] = 0.0f;
+    }
   int unit = 0;        // exponent of the output's current unit
   bool first_unit = true;
-  bool ok = true;
 
   int stage = 0, phase = 0;
   for (int w = warp; w < n_tiles; w += kWarps) {
-    ok = warp_wait(&sh->full[warp][stage], uint32_t(phase), &sh->abort, p.status, kStFull);
-    if (!ok) break;
+    if (!warp_wait(&sh->full[warp][stage], uint32_t(phase), &sh->abort, p.status, kStFull)) break;
     const uint32_t kbase = ring + uint32_t(stage * G_::kStageBytes), vbase = kbase + G_::kTileBytes;
-    const int k0 = w * kTileKeys;
+    const int k0 = w * kTK;
+    if (k0 + kTK > keys || missing) {
+      // zero the keys that are not there
+      for (int i = lane; i < kTK * (D / 16); i += 32) {
+        const int key = i / (D / 16);
+        if (k0 + key >= keys || s_page[(k0 + key) >> ps_log] < 0) {
+          const uint32_t at = swz<D>(key, (i % (D / 16)) * 16);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(kbase + at), "r"(0u) : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vbase + at), "r"(0u) : "memory");
+        }
+      }
+      fence_proxy_async();  // the stage is written by TMA again later
+      __syncwarp();
+    }
 
     // ---- scores ----
-    float sc[4][4];
+    float sc[kMT][NT][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int mt = 0; mt < kMT; ++mt) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[j][e] = 0.0f;
-      const int key = j * 8 + g;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.0f;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        const uint4 v = lds128(kbase + swz<D>(key, t4 * (D / 4) + c * 16));
-        const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
+        const uint4 ka = lds128(kbase + swz<D>(mt * 16 + g, t4 * (D / 4) + c * 16));
+        const uint4 kb = lds128(kbase + swz<D>(mt * 16 + g + 8, t4 * (D / 4) + c * 16));
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mma_f16(sc[j], qf[c * 4 + e], codes_lo(ww[e]), codes_hi(ww[e]));
+        for (int e = 0; e < 4; ++e) {
+          uint32_t a[4];
+          cvt4(wa[e], a[0], a[2]);
+          cvt4(wb[e], a[1], a[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(sc[mt][n], a, qf[n][c * 4 + e][0], qf[n][c * 4 + e][1]);
+        }
       }
     }
-    float mt[2] = {-INFINITY, -INFINITY};
+    const bool masked = k0 + kTK > all_see || missing;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int pg_i = min((k0 + j * 8) / ps, n_pages - 1);
-      const bool there = s_page[pg_i] >= 0;
-      const float pf = exp2i(int(s_scale[pg_i] & 0xFFu) - 127 + 8);
+    for (int mt = 0; mt < kMT; ++mt) {
+      const int pg_i = min((k0 + mt * 16) >> ps_log, n_pages - 1);
+      const float pf = exp2i(int(s_scale[pg_i] & 0xFFu) - 127);
+      const bool there = !missing || s_page[pg_i] >= 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int hh = e >> 1;
-        const int64_t key = k0 + j * 8 + 2 * t4 + (e & 1);
-        const float v = sc[j][e] * (rowf[hh] * pf);
-        sc[j][e] = there && key < vis[hh] ? v : -INFINITY;
-        mt[hh] = fmaxf(mt[hh], sc[j][e]);
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = sc[mt][n][e] * (rowf[n][e & 1] * pf);
+          sc[mt][n][e] = !masked || (there && k0 + mt * 16 + g + 8 * (e >> 1) < vis[n][e & 1]) ? v : -INFINITY;
+        }
+    }
+    float alpha[NT][2], mu[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mt_max = fmaxf(sc[0][n][e], sc[0][n][e + 2]);
+#pragma unroll
+        for (int mt = 1; mt < kMT; ++mt) mt_max = fmaxf(mt_max, fmaxf(sc[mt][n][e], sc[mt][n][e + 2]));
+        mt_max = fmaxf(mt_max, __shfl_xor_sync(0xffffffffu, mt_max, 4));
+        mt_max = fmaxf(mt_max, __shfl_xor_sync(0xffffffffu, mt_max, 8));
+        mt_max = fmaxf(mt_max, __shfl_xor_sync(0xffffffffu, mt_max, 16));
+        const float mn = fmaxf(m[n][e], mt_max);
+        mu[n][e] = mn == -INFINITY ? 0.0f : mn;  // a row that has seen nothing yet
+        alpha[n][e] = fast_exp2(m[n][e] - mu[n][e]);
+        m[n][e] = mn;
+        l[n][e] *= alpha[n][e];
       }
-    }
-    float alpha[2], mu[2];
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      mt[hh] = fmaxf(mt[hh], __shfl_xor_sync(0xffffffffu, mt[hh], 1));
-      mt[hh] = fmaxf(mt[hh], __shfl_xor_sync(0xffffffffu, mt[hh], 2));
-      const float mn = fmaxf(m[hh], mt[hh]);
-      mu[hh] = mn == -INFINITY ? 0.0f : mn;  // a row that has seen nothing yet
-      alpha[hh] = fast_exp2(m[hh] - mu[hh]);
-      m[hh] = mn;
-      l[hh] *= alpha[hh];
-    }
-    uint32_t pr[4][2];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const float a = fast_exp2(sc[j][2 * hh] - mu[hh]), c = fast_exp2(sc[j][2 * hh + 1] - mu[hh]);
-        l[hh] += a + c;
-        pr[j][hh] = h2(a, c);
-      }
-    }
 
-    // ---- output ----
-    float f0 = alpha[0], f1 = alpha[1];
+    // ---- probabilities and output, 16 keys at a time (within one page) ----
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {  // 16 keys each, within one page
-      const int pg_i = min((k0 + st * 16) / ps, n_pages - 1);
+    for (int mt = 0; mt < kMT; ++mt) {
+      const int pg_i = min((k0 + mt * 16) >> ps_log, n_pages - 1);
       const int ev = int(s_scale[pg_i] >> 8) - 127;
       if (ev != unit) {
         if (!first_unit) {
           const float u = exp2i(unit - ev);
-          f0 *= u;
-          f1 *= u;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            alpha[n][0] *= u;
+            alpha[n][1] *= u;
+          }
         }
         unit = ev;
       }
       first_unit = false;
-      if (__any_sync(0xffffffffu, f0 != 1.0f || f1 != 1.0f)) {
+      bool same = true;
 #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-          o[j][0] *= f0;
-          o[j][1] *= f0;
-          o[j][2] *= f1;
-          o[j][3] *= f1;
+      for (int n = 0; n < NT; ++n) same = same && alpha[n][0] == 1.0f && alpha[n][1] == 1.0f;
+      if (!__all_sync(0xffffffffu, same)) {
+#pragma unroll
+        for (int j = 0; j < kS; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[j][n][0] *= alpha[n][0];
+            o[j][n][1] *= alpha[n][1];
+            o[j][n][2] *= alpha[n][0];
+            o[j][n][3] *= alpha[n][1];
+          }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        alpha[n][0] = alpha[n][1] = 1.0f;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float a = fast_exp2(sc[mt][n][2 * hh] - mu[n][0]), c = fast_exp2(sc[mt][n][2 * hh + 1] - mu[n][1]);
+          l[n][0] += a;
+          l[n][1] += c;
+          pb[n][hh] = transpose8(h2(a, c));
         }
       }
-      f0 = f1 = 1.0f;
-      const uint32_t a[4] = {pr[2 * st][0], pr[2 * st][1], pr[2 * st + 1][0], pr[2 * st + 1][1]};
       // this thread's keys 2 t4, + 1, + 8, + 9 and output columns g * D/8 .. + D/8
-      const int key = st * 16 + 2 * t4;
       uint32_t v[4][D / 32];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t at = vbase + swz<D>(key + (i & 1) + 8 * (i >> 1), g * (D / 8));
+        const uint32_t at = vbase + swz<D>(mt * 16 + 2 * t4 + (i & 1) + 8 * (i >> 1), g * (D / 8));
         if constexpr (D == 128) {
           const uint4 x = lds128(at);
           v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
@@ -318,18 +394,20 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       }
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        // byte d of two keys side by side in the high bytes of two halves
+        uint32_t y[4][2];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const uint32_t sel = uint32_t(d << 4) | uint32_t((4 + d) << 12);
-          const uint32_t b0 = codes_hi(__byte_perm(v[0][c], v[1][c], sel));
-          const uint32_t b1 = codes_hi(__byte_perm(v[2][c], v[3][c], sel));
-          mma_f16(o[c * 4 + d], a, b0, b1);
+        for (int i = 0; i < 4; ++i) cvt4(v[i][c], y[i][0], y[i][1]);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const uint32_t a[4] = {__byte_perm(y[0][d], y[1][d], 0x5410), __byte_perm(y[0][d], y[1][d], 0x7632),
+                                 __byte_perm(y[2][d], y[3][d], 0x5410), __byte_perm(y[2][d], y[3][d], 0x7632)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(o[c * 2 + d][n], a, pb[n][0], pb[n][1]);
         }
       }
     }
     __syncwarp();  // every lane has read the stage
-    if (lane == 0 && w + G_::kStages * kWarps < n_tiles) issue(w + G_::kStages * kWarps, stage);
+    if (w + G_::kStages * kWarps < n_tiles) issue(w + G_::kStages * kWarps, stage);
     if (++stage == G_::kStages) {
       stage = 0;
       phase ^= 1;
@@ -338,31 +416,39 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 
   // ---- join the warps ----
 #pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
-    l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
-    l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
-  }
-  const float uf = exp2i(unit + 8);  // out of the page's unit (and the codes' 2^-8)
-  __syncthreads();                   // every warp has left its ring
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+      l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+      l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+    }
+  const float uf = exp2i(unit);  // out of the page's unit
+  __syncthreads();               // every warp has left its ring
   float* so = reinterpret_cast<float*>(smem) + warp * kRowsTile * G_::kOStride;
 #pragma unroll
-  for (int j = 0; j < kN; ++j) {
-    // block j's column n of this thread's fragment is output column n * D/8 + j
-    so[g * G_::kOStride + (2 * t4) * (D / 8) + j] = o[j][0] * uf;
-    so[g * G_::kOStride + (2 * t4 + 1) * (D / 8) + j] = o[j][1] * uf;
-    so[(g + 8) * G_::kOStride + (2 * t4) * (D / 8) + j] = o[j][2] * uf;
-    so[(g + 8) * G_::kOStride + (2 * t4 + 1) * (D / 8) + j] = o[j][3] * uf;
-  }
-  if (t4 == 0) {
-    sh->m[warp][g] = m[0];
-    sh->m[warp][g + 8] = m[1];
-    sh->l[warp][g] = l[0];
-    sh->l[warp][g + 8] = l[1];
+  for (int j = 0; j < kS; ++j)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      // block j's row g is output column g * D/8 + 2 j, its row g + 8 the next one
+      float* x = so + (8 * n + 2 * t4) * G_::kOStride + g * (D / 8) + 2 * j;
+      *reinterpret_cast<float2*>(x) = make_float2(o[j][n][0] * uf, o[j][n][2] * uf);
+      *reinterpret_cast<float2*>(x + G_::kOStride) = make_float2(o[j][n][1] * uf, o[j][n][3] * uf);
+    }
+  if (g == 0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sh->m[warp][8 * n + 2 * t4 + e] = m[n][e];
+        sh->l[warp][8 * n + 2 * t4 + e] = l[n][e];
+      }
   }
   __syncthreads();
   if (*reinterpret_cast<volatile int*>(&sh->abort)) return;
-  constexpr int kPer = D / 8;  // columns of a thread: 8 threads per row
-  const int r = tid >> 3, d0 = (tid & 7) * kPer;
+  constexpr int kTpr = kThreads / kRowsTile;  // threads per row
+  constexpr int kPer = D / kTpr;              // columns of a thread
+  const int r = tid / kTpr, d0 = (tid % kTpr) * kPer;
   if (r >= rows) return;
   float M = -INFINITY;
 #pragma unroll
@@ -382,19 +468,18 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   const int64_t row = (s.t_first + (row0 + r) / G) * p.q_heads + h * G + (row0 + r) % G;
   if (whole) {
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    uint32_t w[kPer / 2];
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + d0);
 #pragma unroll
-    for (int e = 0; e < kPer / 2; ++e) w[e] = pack16(acc[2 * e] * inv, acc[2 * e + 1] * inv, p.fp16);
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + d0);
-#pragma unroll
-    for (int e = 0; e < kPer / 8; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-    if (p.lse != nullptr && (tid & 7) == 0) p.lse[row] = L > 0.0f ? (Mu + log2f(L)) * kLn2 : -INFINITY;
+    for (int e = 0; e < kPer / 2; e += 2)
+      *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack16(acc[2 * e] * inv, acc[2 * e + 1] * inv, p.fp16),
+                                                      pack16(acc[2 * e + 2] * inv, acc[2 * e + 3] * inv, p.fp16));
+    if (p.lse != nullptr && d0 == 0) p.lse[row] = L > 0.0f ? (Mu + log2f(L)) * kLn2 : -INFINITY;
   } else {
     float* dst = p.ws + (row * p.ws_splits + split) * (D + 4);
 #pragma unroll
     for (int e = 0; e < kPer; e += 4)
       *reinterpret_cast<float4*>(dst + d0 + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-    if ((tid & 7) == 0) {
+    if (d0 == 0) {
       dst[D] = M;
       dst[D + 1] = L;
     }
@@ -420,7 +505,7 @@ kv_attn_join_kernel(const KvAttnParams p) {
   const int64_t i = t - __ldg(p.b.cu_new + lo);
   const int64_t n_new = int64_t(__ldg(p.b.cu_new + lo + 1)) - __ldg(p.b.cu_new + lo);
   const bool tc = takes_tc(p, n_new, G);
-  const int tile_rows = tc ? kTcRows : kRowsTile, chunk = tc ? p.tc_chunk : p.chunk;
+  const int tile_rows = tc ? kTcRows : p.tile_rows, chunk = tc ? p.tc_chunk : p.chunk;
   const Rows s = sequence_rows(p, lo, (i * G + hq % G) / tile_rows * tile_rows, tile_rows, G);
   if (i < 0 || i >= s.n || i >= p.max_q_len || s.end <= chunk) return;
   const int n = int((s.end + chunk - 1) / chunk);
@@ -450,23 +535,29 @@ kv_attn_join_kernel(const KvAttnParams p) {
   if (p.lse != nullptr && lane == 0) p.lse[row] = L > 0.0f ? (Mu + log2f(L)) * kLn2 : -INFINITY;
 }
 
+template <int D, int NT>
+cudaError_t launch_rows(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_t stream) {
+  using G_ = Geo<D, NT>;
+  const uint64_t rows128 = uint64_t(p.c.num_pages) * p.c.kv_heads * p.c.page_size * D / 128;
+  const int box = (p.c.page_size < G_::kTileKeys ? p.c.page_size : G_::kTileKeys) * D / 128;
+  CUtensorMap map_k, map_v;
+  if (!encode_bytes_2d(&map_k, p.c.k, rows128, 128, 128, uint32_t(box)) ||
+      !encode_bytes_2d(&map_v, p.c.v, rows128, 128, 128, uint32_t(box)))
+    return cudaErrorInvalidValue;
+  const int pages = p.chunk / p.c.page_size + 1;
+  const int smem = G_::kRing + int(sizeof(Shared)) + pages * 6 + 16 + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = int64_t(plan.row_tiles) * p.c.kv_heads * plan.splits * p.b.num_seqs;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  kv_attn_kernel<D, NT><<<unsigned(grid), kThreads, smem, stream>>>(map_k, map_v, p, plan.row_tiles);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch_attn(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_t stream) {
   if (plan.row_tiles > 0) {
-    const uint64_t rows128 = uint64_t(p.c.num_pages) * p.c.kv_heads * p.c.page_size * D / 128;
-    const int box = (p.c.page_size < kTileKeys ? p.c.page_size : kTileKeys) * D / 128;
-    CUtensorMap map_k, map_v;
-    if (!encode_bytes_2d(&map_k, p.c.k, rows128, 128, 128, uint32_t(box)) ||
-        !encode_bytes_2d(&map_v, p.c.v, rows128, 128, 128, uint32_t(box)))
-      return cudaErrorInvalidValue;
-    const int pages = (p.chunk + p.c.page_size - 1) / p.c.page_size;
-    const int smem = Geo<D>::kRing + int(sizeof(Shared)) + pages * 6 + 16 + 1024;
-    cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const int64_t grid = int64_t(plan.row_tiles) * p.c.kv_heads * plan.splits * p.b.num_seqs;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    kv_attn_kernel<D><<<unsigned(grid), kThreads, smem, stream>>>(map_k, map_v, p, plan.row_tiles);
-    e = cudaGetLastError();
+    const cudaError_t e = p.tile_rows == 8 ? launch_rows<D, 1>(p, plan, stream) : launch_rows<D, 2>(p, plan, stream);
     if (e != cudaSuccess) return e;
   }
   if (p.ws_splits > 1) {
@@ -496,7 +587,8 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
   plan.tc_rows = 64;
   const int64_t few = b.num_seqs == 1 && rows > plan.tc_rows ? 0 : (rows < plan.tc_rows ? rows : plan.tc_rows);
   if (few == 0) plan.tc_rows = 0;  // one sequence: whatever its length, one kernel
-  plan.row_tiles = int((few + kRowsTile - 1) / kRowsTile);
+  plan.tile_rows = few <= 8 ? 8 : 16;
+  plan.row_tiles = int((few + plan.tile_rows - 1) / plan.tile_rows);
   plan.splits = plan.tc_splits = 1;
   plan.chunk = plan.tc_chunk = 0x7FFFFF80;
   if (plan.row_tiles > 0) {
