@@ -38,7 +38,6 @@ using namespace ptx;
 using namespace kv;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kMaxChunk = 8192; // keys of a chunk (its page numbers sit in shared memory)
 
 enum : uint32_t { kStFull = 1u << 0 };
 
@@ -115,6 +114,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   const int H = p.c.kv_heads, G = p.q_heads / H;
   const int ps_log = 31 - __clz(p.c.page_size), ps = 1 << ps_log;
 
+  grid_dependency_launch();
   unsigned idx = blockIdx.x;
   const int tile = int(idx % unsigned(row_tiles));
   idx /= unsigned(row_tiles);
@@ -486,15 +486,20 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   }
 }
 
-// Joins the chunks of the rows that had more than one: a warp per row.
-template <int D>
-__global__ void __launch_bounds__(128)
+// Joins the chunks of the rows that had more than one. D / 4 threads lie side by side on a row's
+// columns; kWide: a CTA takes one row, its groups of D / 4 threads different chunks of it (few rows
+// with hundreds of chunks: a group alone took longer than the attention itself); else every group
+// has a row of its own (many rows with a few chunks).
+template <int D, bool kWide>
+__global__ void __launch_bounds__(kThreads)
 kv_attn_join_kernel(const KvAttnParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  constexpr int kCols = D / 4, kGroups = kThreads / kCols;
+  const int tid = threadIdx.x;
+  const int col = tid % kCols, grp = tid / kCols;
+  const int64_t row = kWide ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * kGroups + grp;
   if (row >= p.T * p.q_heads) return;
   const int64_t t = row / p.q_heads;
-  const int hq = int(row % p.q_heads);
+  const int hq = int(row - t * p.q_heads);
   int lo = 0, hi = p.b.num_seqs - 1;  // the last sequence that starts at or before t
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -510,29 +515,54 @@ kv_attn_join_kernel(const KvAttnParams p) {
   if (i < 0 || i >= s.n || i >= p.max_q_len || s.end <= chunk) return;
   const int n = int((s.end + chunk - 1) / chunk);
   const float* src = p.ws + row * p.ws_splits * (D + 4);
-  float M = -INFINITY;
-  for (int c = lane; c < n; c += 32) M = fmaxf(M, src[int64_t(c) * (D + 4) + D]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float Mu = M == -INFINITY ? 0.0f : M;
-  constexpr int E = D / 32;
-  float L = 0.0f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+  grid_dependency_wait();  // the chunks' results
+  // a running maximum, as in the chunks themselves
+  float M = -INFINITY, L = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (int c = 0; c < n; ++c) {
+  for (int c = kWide ? grp : 0; c < n; c += kWide ? kGroups : 1) {
     const float* x = src + int64_t(c) * (D + 4);
-    const float f = fast_exp2(x[D] - Mu);
-    L += x[D + 1] * f;
+    const float m = x[D], l = x[D + 1];
+    const float4 v = *reinterpret_cast<const float4*>(x + 4 * col);
+    const float mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.0f : mn;
+    const float f = fast_exp2(m - mu), g = fast_exp2(M - mu);
+    M = mn;
+    L = L * g + l * f;
+    acc.x = acc.x * g + v.x * f;
+    acc.y = acc.y * g + v.y * f;
+    acc.z = acc.z * g + v.z * f;
+    acc.w = acc.w * g + v.w * f;
+  }
+  if constexpr (kWide) {
+    __shared__ float s_m[kGroups], s_l[kGroups];
+    __shared__ float4 s_o[kGroups][kCols];
+    if (col == 0) {
+      s_m[grp] = M;
+      s_l[grp] = L;
+    }
+    s_o[grp][col] = acc;
+    __syncthreads();
+    if (grp != 0) return;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += x[lane * E + e] * f;
+    for (int k = 1; k < kGroups; ++k) M = fmaxf(M, s_m[k]);
+    const float mu = M == -INFINITY ? 0.0f : M;
+    L = 0.0f;
+    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const float4 v = s_o[k][col];
+      const float f = fast_exp2(s_m[k] - mu);
+      L += s_l[k] * f;
+      acc.x += v.x * f;
+      acc.y += v.y * f;
+      acc.z += v.z * f;
+      acc.w += v.w * f;
+    }
   }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack16(acc[e] * inv, acc[e + 1] * inv, p.fp16);
-  if (p.lse != nullptr && lane == 0) p.lse[row] = L > 0.0f ? (Mu + log2f(L)) * kLn2 : -INFINITY;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + 4 * col) =
+      make_uint2(pack16(acc.x * inv, acc.y * inv, p.fp16), pack16(acc.z * inv, acc.w * inv, p.fp16));
+  if (p.lse != nullptr && col == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 template <int D, int NT>
@@ -561,11 +591,24 @@ cudaError_t launch_attn(const KvAttnParams& p, const KvAttnPlan& plan, cudaStrea
     if (e != cudaSuccess) return e;
   }
   if (p.ws_splits > 1) {
-    const int64_t blocks = (p.T * p.q_heads + 3) / 4;
+    // launched with the attention kernel still running (its blocks wait for it to complete)
+    const int64_t rows = p.T * p.q_heads;
+    const bool wide = p.ws_splits > 8;
+    const int64_t blocks = wide ? rows : (rows + kThreads / (D / 4) - 1) / (kThreads / (D / 4));
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    kv_attn_join_kernel<D><<<unsigned(blocks), 128, 0, stream>>>(p);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(blocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return wide ? cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<D, true>, p)
+                : cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<D, false>, p);
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 // Chunk of keys for `ctas` CTAs of one chunk each over max_len keys: chunks until there are
@@ -593,7 +636,10 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
   plan.chunk = plan.tc_chunk = 0x7FFFFF80;
   if (plan.row_tiles > 0) {
     const int64_t ctas = int64_t(b.num_seqs) * c.kv_heads * plan.row_tiles;
-    plan.chunk = int(chunk_for(max_seq_len, ctas, 4 * int64_t(num_sms), 256, kMaxChunk));
+    // the machine filled once (three CTAs on an SM), or chunks of 1 MB, whichever is smaller: a
+    // ragged batch then ends evenly (64 sequences of 500-16000: 197 us with chunks of 2 MB, 182 with
+    // 1 MB), and a CTA's start and end (about 3 us) and the join stay small beside its chunk
+    plan.chunk = int(chunk_for(max_seq_len, ctas, 3 * int64_t(num_sms), 256, 4096 * 128 / c.head_dim));
     plan.splits = int((max_seq_len + plan.chunk - 1) / plan.chunk);
   }
   if (rows > plan.tc_rows) {

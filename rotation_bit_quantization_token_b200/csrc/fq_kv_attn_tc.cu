@@ -206,6 +206,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const int ps = p.c.page_size, H = p.c.kv_heads, G = p.q_heads / H;
 
   // the longest (last) row tiles first, so that the short ones fill the end of the launch
+  grid_dependency_launch();
   unsigned idx = blockIdx.x;
   const int h = int(idx % unsigned(H));
   idx /= unsigned(H);

@@ -14,6 +14,11 @@ namespace fq {
 namespace kv {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// A kernel launched with programmatic serialization may start before the one ahead of it ends: the
+// first tells that its dependents may be launched, the second waits until it has completed.
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float fast_exp2(float x) {
