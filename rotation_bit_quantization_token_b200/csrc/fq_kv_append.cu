@@ -11,11 +11,17 @@
 // is found without the host: a sequence with n new tokens touches at most n / page_size + 2
 // pages, so with start(b) = cu_new[b] / page_size + 2b the items of sequence b are start(b),
 // start(b) + 1, ... and T / page_size + 2 num_seqs CTAs cover every batch; CTAs past a
-// sequence's last page leave at once. sin and cos of the page's tokens are computed once per
-// CTA (angle and reduction in float64: pos * inv_freq needs up to 48 bits) and serve all its
-// heads. A warp carries up to kRows rows of one head in registers between the maximum and the
-// encoding, so the inputs are read once; a page with more rows is shared by several warps,
-// which meet in shared memory for the maximum.
+// sequence's last page leave at once. (The search is 32 probes at a time: one by one it was most of
+// a decode step's time.) sin and cos of the page's tokens are computed once per CTA (angle and
+// reduction in float64: pos * inv_freq needs up to 48 bits) and serve all its heads.
+//
+// A lane holds four elements of a row, chosen so that it has both of each pair that is turned
+// (elements d, d + 1 and their partners half the rotated part further on, or four neighbours), so
+// every element is read once. A warp carries its rows of one head in registers between the maximum
+// and the encoding; a page with more rows is shared by several warps, which meet in shared memory
+// for the maximum. Queries need no page: the CTAs behind those of the items take them, a warp for
+// one token and up to eight heads. The kernel is bound by reading 2 bytes and writing 1 byte an element of k and v
+// (2 and 2 for q).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -29,7 +35,6 @@ namespace fq {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRows = 16;  // rows of a task in one warp's registers
 
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t w);
@@ -54,19 +59,6 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// E elements (2 or 4) at p, as float32
-template <typename T, int E>
-__device__ __forceinline__ void load_elems(const T* p, float* x) {
-  if constexpr (E == 4) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-    const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y);
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-  } else {
-    const float2 a = unpack2<T>(__ldg(reinterpret_cast<const uint32_t*>(p)));
-    x[0] = a.x; x[1] = a.y;
-  }
-}
-
 // Two floats as E4M3 bytes (nearest even, saturating), a in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
@@ -86,63 +78,140 @@ __device__ __forceinline__ int page_exponent(float amax) {
   return e > kPageExpMax ? kPageExpMax : e;
 }
 
-// The E elements d0 .. d0 + E - 1 of one head's row, rotated. cs: (cos, sin) of the row's pairs.
-template <typename T, int D, int E>
-__device__ __forceinline__ void load_rotated(const T* row, int d0, const float2* cs, int rot, int interleaved,
-                                             float* x) {
-  load_elems<T, E>(row + d0, x);
-  if (d0 >= rot) return;  // rot is a multiple of E
-  if (interleaved) {
+// A lane's four elements of a row: lo, lo + 1, hi, hi + 1.
+struct Quad {
+  int lo, hi;
+  bool turned;    // the pairs are turned: (lo, hi) and (lo + 1, hi + 1), or neighbours if interleaved
+};
+__device__ __forceinline__ Quad quad_of(int q, int rot, int interleaved) {
+  const int half = rot >> 1;
+  Quad z;
+  z.lo = 4 * q;
+  z.hi = 4 * q + 2;
+  z.turned = 4 * q < rot;
+  if (!interleaved && z.turned) {
+    z.lo = 2 * q;
+    z.hi = half + 2 * q;
+  }
+  return z;  // lanes past rot / 4 hold the elements from rot on, four each
+}
+
+template <typename T>
+__device__ __forceinline__ uint2 load_quad(const T* row, const Quad& z) {
+  if (z.hi == z.lo + 2) return __ldg(reinterpret_cast<const uint2*>(row + z.lo));
+  return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row + z.lo)), __ldg(reinterpret_cast<const uint32_t*>(row + z.hi)));
+}
+
+// cs: (cos, sin) of the quad's two pairs
+template <typename T>
+__device__ __forceinline__ float4 turn(uint2 w, const Quad& z, int interleaved, float4 cs) {
+  const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y);
+  if (!z.turned) return make_float4(a.x, a.y, b.x, b.y);
+  if (interleaved)
+    return make_float4(a.x * cs.x - a.y * cs.y, a.y * cs.x + a.x * cs.y, b.x * cs.z - b.y * cs.w, b.y * cs.z + b.x * cs.w);
+  return make_float4(a.x * cs.x - b.x * cs.y, a.y * cs.z - b.y * cs.w, b.x * cs.x + a.x * cs.y, b.y * cs.z + a.y * cs.w);
+}
+
+// (cos, sin) of angle pos * f: turns = pos * f / (2 pi); the fraction of a turn is exact to 2^-52 of
+// the turns.
+__device__ __forceinline__ float2 cos_sin_of(int64_t pos, float f) {
+  const double turns = double(pos) * double(f) * 0.15915494309189533577;
+  float s, c;
+  sincospif(float(2.0 * (turns - rint(turns))), &s, &c);
+  return make_float2(c, s);
+}
+
+// The last b in [0, n) with key(b) <= x, keys rising, key(0) <= x assumed: 32 probes at a time, by a
+// whole warp.
+template <typename F>
+__device__ __forceinline__ int warp_search(int n, int x, const F& key) {
+  const int lane = threadIdx.x & 31;
+  int b = 0;
+  for (int left = n; left > 1;) {  // it is one of b .. b + left - 1
+    const int step = (left + 31) >> 5;
+    const bool in = lane * step < left && key(b + lane * step) <= x;
+    const int top = 31 - __clz(__ballot_sync(0xffffffffu, in) | 1u);
+    b += top * step;
+    left = min(step, left - top * step);
+  }
+  return b;
+}
+
+constexpr int kQHeads = 8;  // query heads of one token that a warp takes
+
+// Queries: warp `task` takes heads kQHeads * (task % chunks) .. of token task / chunks.
+template <typename T, int D>
+__device__ __forceinline__ void rotate_queries(const KvAppendParams& p, int64_t task) {
+  constexpr int kLpr = D / 4, kRps = 32 / kLpr;  // lanes per row, rows per step of a warp
+  constexpr int kIter = kQHeads / kRps;
+  const int lane = threadIdx.x & 31, lq = lane % kLpr, sub = lane / kLpr;
+  const int chunks = (p.q_heads + kQHeads - 1) / kQHeads;
+  const int64_t t = task / chunks;
+  const int h0 = int(task - t * chunks) * kQHeads;
+  if (t >= p.T) return;
+  const Quad z = quad_of(lq, p.rot_dim, p.interleaved);
+  uint2 w[kIter];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 z = cs[(d0 + e) >> 1];
-      const float a = x[e], b = x[e + 1];
-      x[e] = a * z.x - b * z.y;
-      x[e + 1] = b * z.x + a * z.y;
-    }
-  } else {
-    const int half = rot >> 1;
-    const bool low = d0 < half;
-    float y[E];
-    load_elems<T, E>(row + (low ? d0 + half : d0 - half), y);
+  for (int k = 0; k < kIter; ++k) {
+    const int h = h0 + k * kRps + sub;
+    w[k] = make_uint2(0u, 0u);
+    if (h < p.q_heads) w[k] = load_quad(static_cast<const T*>(p.q) + t * p.q_stride + int64_t(h) * D, z);
+  }
+  const int b = warp_search(p.b.num_seqs, int(t), [&](int i) { return __ldg(p.b.cu_new + i); });
+  const int64_t t_first = __ldg(p.b.cu_new + b), t_end = __ldg(p.b.cu_new + b + 1), len = __ldg(p.b.seq_lens + b);
+  const int64_t pos = len - (t_end - t);
+  if (t < t_first || t >= t_end || t_first < 0 || t_end > p.T || len < t_end - t_first) return;  // no sequence's token
+  float4 cs = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+  if (z.turned) {
+    const float2 f = *reinterpret_cast<const float2*>(p.inv_freq + 2 * lq);
+    const float2 a = cos_sin_of(pos, f.x), c = cos_sin_of(pos, f.y);
+    cs = make_float4(a.x, a.y, c.x, c.y);
+  }
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float2 z = cs[(low ? d0 : d0 - half) + e];
-      x[e] = low ? x[e] * z.x - y[e] * z.y : x[e] * z.x + y[e] * z.y;
+  for (int k = 0; k < kIter; ++k) {
+    const int h = h0 + k * kRps + sub;
+    if (h >= p.q_heads) continue;
+    const float4 x = turn<T>(w[k], z, p.interleaved, cs);
+    T* dst = static_cast<T*>(p.q_out) + (t * p.q_heads + h) * D;
+    if (z.hi == z.lo + 2) {
+      *reinterpret_cast<uint2*>(dst + z.lo) = make_uint2(pack2<T>(x.x, x.y), pack2<T>(x.z, x.w));
+    } else {
+      *reinterpret_cast<uint32_t*>(dst + z.lo) = pack2<T>(x.x, x.y);
+      *reinterpret_cast<uint32_t*>(dst + z.hi) = pack2<T>(x.z, x.w);
     }
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
-kv_append_kernel(const KvAppendParams p) {
-  constexpr int E = D / 32;  // elements of a row per lane
+template <typename T, int D, int kSteps>
+__global__ void __launch_bounds__(kThreads, kSteps == 8 ? 4 : 2)
+kv_append_kernel(const KvAppendParams p, const unsigned kv_ctas, const unsigned groups) {
+  constexpr int kLpr = D / 4, kRps = 32 / kLpr;  // lanes per row, rows per step of a warp
+  constexpr int kWarpRows = kSteps * kRps;
   extern __shared__ float2 s_cs[];  // [rows][rot / 2]
   __shared__ float s_max[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ps = p.c.page_size, H = p.c.kv_heads;
-
-  // ---- the work item ----
-  const int item = blockIdx.x;
-  int lo = 0, hi = p.b.num_seqs - 1;  // the last sequence with start(b) <= item
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (int64_t(__ldg(p.b.cu_new + mid)) / ps + 2 * int64_t(mid) <= item) lo = mid;
-    else hi = mid - 1;
+  if (blockIdx.x >= kv_ctas) {
+    rotate_queries<T, D>(p, int64_t(blockIdx.x - kv_ctas) * kWarps + warp);
+    return;
   }
-  const int b = lo;
+  const int H = p.c.kv_heads;
+  const int ps_log = 31 - __clz(p.c.page_size), ps = 1 << ps_log;
+
+  // ---- the work item: the last sequence with start(b) <= item ----
+  const int item = int(blockIdx.x / groups), group = int(blockIdx.x - unsigned(item) * groups);
+  const int b = warp_search(p.b.num_seqs, item, [&](int i) { return (__ldg(p.b.cu_new + i) >> ps_log) + 2 * i; });
   const int64_t t_first = __ldg(p.b.cu_new + b);
   const int64_t n = int64_t(__ldg(p.b.cu_new + b + 1)) - t_first;
   const int64_t len = __ldg(p.b.seq_lens + b);
   const int64_t first = len - n;  // position of the first new token
-  const int64_t local = int64_t(item) - (t_first / ps + 2 * int64_t(b));
+  const int64_t local = int64_t(item) - ((t_first >> ps_log) + 2 * int64_t(b));
   if (n <= 0 || local < 0) return;
   if (first < 0 || t_first < 0 || t_first + n > p.T) {
-    if (local == 0 && tid == 0 && p.status != nullptr) atomicOr(p.status, FQ_KV_BAD_BATCH);
+    if (tid == 0 && p.status != nullptr) atomicOr(p.status, FQ_KV_BAD_BATCH);
     return;
   }
-  const int64_t page_idx = first / ps + local;
-  const int64_t at0 = page_idx * ps;
+  const int64_t page_idx = (first >> ps_log) + local;
+  const int64_t at0 = page_idx << ps_log;
   if (at0 >= len) return;
   const int r0 = first > at0 ? int(first - at0) : 0;  // rows r0 .. r1 - 1 of the page are new
   const int r1 = len - at0 < ps ? int(len - at0) : ps;
@@ -157,21 +226,21 @@ kv_append_kernel(const KvAppendParams p) {
   const int half = p.rot_dim >> 1;
   for (int i = tid; i < rows * half; i += kThreads) {
     const int r = i / half, j = i - r * half;
-    // turns = pos * f / (2 pi); the fraction of a turn is exact to 2^-52 of the turns
-    const double turns = double(at0 + r0 + r) * double(__ldg(p.inv_freq + j)) * 0.15915494309189533577;
-    float s, c;
-    sincospif(float(2.0 * (turns - rint(turns))), &s, &c);
-    s_cs[i] = make_float2(c, s);
+    s_cs[i] = cos_sin_of(at0 + r0 + r, __ldg(p.inv_freq + j));
   }
   __syncthreads();
 
-  const int h_begin = blockIdx.y * p.heads_per_cta;
+  const int h_begin = group * p.heads_per_cta;
   const int h_end = min(h_begin + p.heads_per_cta, H);
-  const int d0 = lane * E;
+  const int lq = lane % kLpr, sub = lane / kLpr;
+  const Quad kz = quad_of(lq, p.rot_dim, p.interleaved), vz = quad_of(lq, 0, 1);
+  auto cos_sin = [&](int r) {
+    return kz.turned ? *reinterpret_cast<const float4*>(s_cs + r * half + 2 * lq) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+  };
 
   // ---- keys and values: a task is one head of K or of V; wpt warps share it ----
   int wpt = 1;
-  while (wpt * kRows < rows) wpt *= 2;
+  while (wpt * kWarpRows < rows) wpt *= 2;
   const int tasks = stored ? 2 * (h_end - h_begin) : 0;
   const int per_round = kWarps / wpt;
   for (int base = 0; base < tasks; base += per_round) {
@@ -179,23 +248,28 @@ kv_append_kernel(const KvAppendParams p) {
     const bool active = task < tasks;
     const int h = h_begin + (task >> 1);
     const bool is_k = (task & 1) == 0;
-    float x[kRows][E];
+    const Quad z = is_k ? kz : vz;
+    float4 x[kSteps];
     float m = 0.0f;
     int old = 0;  // exponent of the page's older rows
     uint8_t* scale = (is_k ? p.c.k_scale : p.c.v_scale) + int64_t(page) * H + h;
     if (active) {
-      if (r0 > 0) old = int(*scale) - 127;
       const int64_t stride = is_k ? p.k_stride : p.v_stride;
       const T* src = static_cast<const T*>(is_k ? p.k : p.v) + t0 * stride + int64_t(h) * D;
+      uint2 w[kSteps];
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int r = part + i * wpt;
-        if (r < rows) {
-          if (is_k) load_rotated<T, D, E>(src + r * stride, d0, s_cs + r * half, p.rot_dim, p.interleaved, x[i]);
-          else load_elems<T, E>(src + r * stride + d0, x[i]);
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = (part + i * wpt) * kRps + sub;
+        w[i] = make_uint2(0u, 0u);
+        if (r < rows) w[i] = load_quad(src + r * stride, z);
+      }
+      if (r0 > 0) old = int(*scale) - 127;
 #pragma unroll
-          for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(x[i][e]));
-        }
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = (part + i * wpt) * kRps + sub;
+        x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < rows) x[i] = turn<T>(w[i], z, p.interleaved, is_k ? cos_sin(r) : make_float4(1.0f, 0.0f, 1.0f, 0.0f));
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w))));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -226,60 +300,56 @@ kv_append_kernel(const KvAppendParams p) {
     }
     const float f = ptx::exp2i(-e);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int r = part + i * wpt;
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = (part + i * wpt) * kRps + sub;
       if (r < rows) {
-        uint8_t* dst = codes + (r0 + r) * D + d0;
-        const uint32_t w = e4m3x2(x[i][0] * f, x[i][1] * f);
-        if constexpr (E == 4)
-          *reinterpret_cast<uint32_t*>(dst) = w | (e4m3x2(x[i][2] * f, x[i][3] * f) << 16);
-        else
-          *reinterpret_cast<uint16_t*>(dst) = uint16_t(w);
+        uint8_t* dst = codes + (r0 + r) * D;
+        const uint32_t lo = e4m3x2(x[i].x * f, x[i].y * f), hi = e4m3x2(x[i].z * f, x[i].w * f);
+        if (z.hi == z.lo + 2) {
+          *reinterpret_cast<uint32_t*>(dst + z.lo) = lo | (hi << 16);
+        } else {
+          *reinterpret_cast<uint16_t*>(dst + z.lo) = uint16_t(lo);
+          *reinterpret_cast<uint16_t*>(dst + z.hi) = uint16_t(hi);
+        }
       }
     }
     if (part == 0 && lane == 0) *scale = uint8_t(e + 127);
   }
 
-  // ---- queries ----
-  if (p.q != nullptr) {
-    const int G = p.q_heads / H;
-    const int nh = (h_end - h_begin) * G;
-    for (int i = warp; i < rows * nh; i += kWarps) {
-      const int r = i / nh, h = h_begin * G + i % nh;
-      float x[E];
-      load_rotated<T, D, E>(static_cast<const T*>(p.q) + (t0 + r) * p.q_stride + int64_t(h) * D, d0, s_cs + r * half,
-                            p.rot_dim, p.interleaved, x);
-      T* dst = static_cast<T*>(p.q_out) + ((t0 + r) * p.q_heads + h) * D + d0;
-      if constexpr (E == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
-      else
-        *reinterpret_cast<uint32_t*>(dst) = pack2<T>(x[0], x[1]);
-    }
-  }
 }
 
-template <typename T, int D>
-cudaError_t launch_append(const KvAppendParams& p0, int num_sms, cudaStream_t stream) {
+template <typename T, int D, int kSteps>
+cudaError_t launch_steps(const KvAppendParams& p0, int num_sms, cudaStream_t stream) {
   KvAppendParams p = p0;
   const int64_t items = p.T / p.c.page_size + 2 * int64_t(p.b.num_seqs);
-  // heads are divided among CTAs until every SM has about four of them
+  // heads are divided among CTAs until every SM has about eight of them
   int groups = 1;
-  while (groups < p.c.kv_heads && items * groups < 4 * int64_t(num_sms)) groups *= 2;
+  while (groups < p.c.kv_heads && items * groups < 8 * int64_t(num_sms)) groups *= 2;
   p.heads_per_cta = (p.c.kv_heads + groups - 1) / groups;
   groups = (p.c.kv_heads + p.heads_per_cta - 1) / p.heads_per_cta;
   const int smem = p.c.page_size * (p.rot_dim / 2) * int(sizeof(float2));
-  cudaError_t e = cudaFuncSetAttribute(kv_append_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kern = kv_append_kernel<T, D, kSteps>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kv_append_kernel<T, D><<<dim3(unsigned(items), unsigned(groups)), kThreads, smem, stream>>>(p);
+  const int64_t q_tasks = p.q != nullptr ? p.T * ((p.q_heads + kQHeads - 1) / kQHeads) : 0;
+  const int64_t kv_ctas = items * groups, ctas = kv_ctas + (q_tasks + kWarps - 1) / kWarps;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  kern<<<unsigned(ctas), kThreads, smem, stream>>>(p, unsigned(kv_ctas), unsigned(groups));
   return cudaGetLastError();
+}
+
+// A CTA's warps hold 8 * 8 rows of 128 elements, or 8 * 16 of 64: a page of 128 rows of 128 needs
+// twice the steps (and registers).
+template <typename T>
+cudaError_t launch_type(const KvAppendParams& p, int num_sms, cudaStream_t stream) {
+  if (p.c.head_dim == 64) return launch_steps<T, 64, 8>(p, num_sms, stream);
+  return p.c.page_size == 128 ? launch_steps<T, 128, 16>(p, num_sms, stream) : launch_steps<T, 128, 8>(p, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendParams& p, bool fp16, int num_sms, cudaStream_t stream) {
-  if (p.c.head_dim == 128)
-    return fp16 ? launch_append<__half, 128>(p, num_sms, stream) : launch_append<__nv_bfloat16, 128>(p, num_sms, stream);
-  return fp16 ? launch_append<__half, 64>(p, num_sms, stream) : launch_append<__nv_bfloat16, 64>(p, num_sms, stream);
+  return fp16 ? launch_type<__half>(p, num_sms, stream) : launch_type<__nv_bfloat16>(p, num_sms, stream);
 }
 
 }  // namespace fq
