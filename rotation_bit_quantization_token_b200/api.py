@@ -16,8 +16,21 @@ _OUT_DT = {**_DT, torch.float32: _lib.FQ_FP32}
 
 
 def _stream_ptr(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+
+
+def _raw_stream(stream, device):
+    """The stream's handle as a number (the current one of `device` unless given)."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+
+
+def _fits(t, dtype, device):
+    """Whether t is a contiguous tensor of this type on this CUDA device: the checks of a call
+    that is in order. (A call that is not goes through the ones below, which say what is
+    wrong.)"""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
 
 
 def _ptr(t):
@@ -254,28 +267,35 @@ def int8_matmul(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stat
     float16 or float32. status: an int32 tensor of one element, ORed with a nonzero code if a
     bounded wait inside the kernel gives up (the output is then undefined)."""
     lib = _lib.load()
-    for name, t, dt, dims in (("a", a, torch.int8, 2), ("a_scale", a_scale, torch.float32, 1),
-                              ("w", w, torch.int8, 2), ("w_scale", w_scale, torch.float32, 1)):
-        _check_input(name, t, dt)
+    dev = torch.cuda.current_device() if isinstance(a, torch.Tensor) and a.is_cuda else -1
+    if not (dev >= 0 and _fits(a, torch.int8, dev) and _fits(a_scale, torch.float32, dev) and _fits(w, torch.int8, dev)
+            and _fits(w_scale, torch.float32, dev)):
+        for name, t, dt in (("a", a, torch.int8), ("a_scale", a_scale, torch.float32), ("w", w, torch.int8),
+                            ("w_scale", w_scale, torch.float32)):
+            _check_input(name, t, dt)
+        _check_device(a, a_scale=a_scale, w=w, w_scale=w_scale)
+    for name, t, dims in (("a", a, 2), ("a_scale", a_scale, 1), ("w", w, 2), ("w_scale", w_scale, 1)):
         if t.dim() != dims:
             raise ValueError(f"{name} must have {dims} dimension{'s' if dims > 1 else ''}")
     if out_dtype not in _OUT_DT:
         raise ValueError("out_dtype must be torch.bfloat16, torch.float16 or torch.float32")
     T, L = a.shape
-    O = w.shape[0]
-    if w.shape[1] != L:
-        raise ValueError(f"w must have rows of {L} codes, got {w.shape[1]}")
+    O, Lw = w.shape
+    if Lw != L:
+        raise ValueError(f"w must have rows of {L} codes, got {Lw}")
     if a_scale.numel() != T or w_scale.numel() != O:
         raise ValueError("a_scale and w_scale must have one scale per row of a and of w")
-    _check_device(a, a_scale=a_scale, w=w, w_scale=w_scale)
     if out is None:
         out = torch.empty((T, O), dtype=out_dtype, device=a.device)
     else:
         _check_output("out", out, T * O * out_dtype.itemsize, a.device, out_dtype)
     if status is not None:
         _check_output("status", status, 4, a.device, torch.int32)
-    _lib.check(lib.fq_int8_matmul(T, O, L, _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _OUT_DT[out_dtype],
-                                  _ptr(out), _ptr(status), _stream_ptr(stream)), "fq_int8_matmul")
+    st = lib.fq_int8_matmul(T, O, L, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                            _OUT_DT[out_dtype], out.data_ptr(), status.data_ptr() if status is not None else None,
+                            _raw_stream(stream, dev))
+    if st != _lib.FQ_OK:
+        _lib.check(st, "fq_int8_matmul")
     return out
 
 
@@ -319,10 +339,20 @@ class KVCache:
             raise ValueError(f"page_size must be 16, 32, 64 or 128, got {k.shape[2]}")
         if k.shape[3] not in (64, 128):
             raise ValueError(f"head_dim must be 64 or 128, got {k.shape[3]}")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = (k, v, k_scale, v_scale)
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self._device = k.get_device()
         self._status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._status_ptr = self._status.data_ptr()
         self._lib = _lib.load()
+        self._desc = _lib.KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                      self.num_pages, self.kv_heads, self.page_size, self.head_dim)
+        self._workspace_bytes = {}  # by the sizes that decide it
+
+    k = property(lambda self: self._tensors[0], doc="E4M3 codes of the keys")
+    v = property(lambda self: self._tensors[1], doc="E4M3 codes of the values")
+    k_scale = property(lambda self: self._tensors[2], doc="E8M0 bytes of the keys")
+    v_scale = property(lambda self: self._tensors[3], doc="E8M0 bytes of the values")
 
     def device_status(self):
         """Reads and clears the cache's status word: 0, or the bits that calls on this cache have
@@ -332,14 +362,13 @@ class KVCache:
             self._status.zero_()
         return v
 
-    def _cache_desc(self):
-        return _lib.KvCacheDesc(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
-                                self.v_scale.data_ptr(), self.num_pages, self.kv_heads, self.page_size,
-                                self.head_dim)
-
     def _batch_desc(self, cu_new, seq_lens, page_table):
-        for name, t in (("cu_new", cu_new), ("seq_lens", seq_lens), ("page_table", page_table)):
-            _check_input(name, t, torch.int32)
+        dev = self._device
+        if not (_fits(cu_new, torch.int32, dev) and _fits(seq_lens, torch.int32, dev)
+                and _fits(page_table, torch.int32, dev)):
+            for name, t in (("cu_new", cu_new), ("seq_lens", seq_lens), ("page_table", page_table)):
+                _check_input(name, t, torch.int32)
+            _check_device(self.k, cu_new=cu_new, seq_lens=seq_lens, page_table=page_table)
         B = seq_lens.numel()
         if seq_lens.dim() != 1 or cu_new.dim() != 1 or cu_new.numel() != B + 1:
             raise ValueError("seq_lens must be [B] and cu_new [B + 1]")
@@ -352,16 +381,27 @@ class KVCache:
         """A token array [T, heads, head_dim]: heads contiguous, any distance between tokens."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (libfq has no CPU path)")
+        if t.get_device() != self._device:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor (libfq has no CPU path)")
+            raise ValueError(f"{name} must be on {self.k.device}, got {t.device}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
         D = self.head_dim
-        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
-            raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
-        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+        shape = t.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != D or (heads is not None and shape[1] != heads):
+            raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}], got {tuple(shape)}")
+        s0, s1, s2 = t.stride()
+        if s2 != 1 or (shape[1] > 1 and s1 != D):
             raise ValueError(f"the heads of one token of {name} must be contiguous")
-        return t.stride(0) if T > 1 else t.shape[1] * D
+        return s0 if T > 1 else shape[1] * D
+
+    def _check_current(self):
+        """The cache on the current CUDA device, where its kernels are launched."""
+        cur = torch.cuda.current_device()
+        if self._device != cur:
+            raise ValueError(f"the cache is on {self.k.device} but the current CUDA device is cuda:{cur}; "
+                             "call torch.cuda.set_device first")
 
     def append(self, k, v, cu_new, seq_lens, page_table, q=None, inv_freq=None, interleaved=False, q_out=None,
                stream=None):
@@ -370,31 +410,32 @@ class KVCache:
         their positions first (see fq_kv_append). Returns the rotated queries, or None."""
         if not isinstance(k, torch.Tensor) or k.dtype not in _DT:
             raise ValueError("k must be a bfloat16 or float16 tensor")
-        T = k.shape[0]
+        self._check_current()
+        T = k.shape[0] if k.dim() else 0
         ks = self._tokens("k", k, T, self.kv_heads, k.dtype)
         vs = self._tokens("v", v, T, self.kv_heads, k.dtype)
         batch = self._batch_desc(cu_new, seq_lens, page_table)
-        rot, qs, hq = 0, 0, 0
+        rot, freq, qs, hq, q_ptr, out_ptr = 0, None, 0, 0, None, None
         if inv_freq is not None:
-            _check_input("inv_freq", inv_freq, torch.float32)
-            rot = 2 * inv_freq.numel()
+            if not _fits(inv_freq, torch.float32, self._device):
+                _check_input("inv_freq", inv_freq, torch.float32)
+                _check_device(self.k, inv_freq=inv_freq)
+            rot, freq = 2 * inv_freq.numel(), inv_freq.data_ptr()
         if q is not None:
             qs = self._tokens("q", q, T, None, k.dtype)
             hq = q.shape[1]
-        _check_device(k, cache=self.k, v=v, q=q, cu_new=cu_new, seq_lens=seq_lens, page_table=page_table,
-                      inv_freq=inv_freq)
-        if q is None:
-            if q_out is not None:
-                raise ValueError("q_out needs q")
-        elif q_out is None:
-            q_out = torch.empty((T, hq, self.head_dim), dtype=q.dtype, device=q.device)
-        else:
-            _check_output("q_out", q_out, T * hq * self.head_dim * 2, q.device, q.dtype)
-        cache = self._cache_desc()
-        _lib.check(self._lib.fq_kv_append(
-            ctypes.byref(cache), ctypes.byref(batch), T, _DT[k.dtype], _ptr(k), ks, _ptr(v), vs, _ptr(inv_freq), rot,
-            int(bool(interleaved)), _ptr(q), qs, hq, _ptr(q_out), _ptr(self._status), _stream_ptr(stream)),
-            "fq_kv_append")
+            if q_out is None:
+                q_out = torch.empty((T, hq, self.head_dim), dtype=q.dtype, device=q.device)
+            else:
+                _check_output("q_out", q_out, T * hq * self.head_dim * 2, q.device, q.dtype)
+            q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out needs q")
+        st = self._lib.fq_kv_append(
+            ctypes.byref(self._desc), ctypes.byref(batch), T, _DT[k.dtype], k.data_ptr(), ks, v.data_ptr(), vs, freq,
+            rot, 1 if interleaved else 0, q_ptr, qs, hq, out_ptr, self._status_ptr, _raw_stream(stream, self._device))
+        if st != _lib.FQ_OK:
+            _lib.check(st, "fq_kv_append")
         return q_out
 
     def attention(self, q, cu_new, seq_lens, page_table, max_q_len, max_seq_len=None, scale=None, causal=True,
@@ -405,13 +446,13 @@ class KVCache:
         unless given. Returns out, or (out, lse [T, q_heads] float32) with return_lse."""
         if not isinstance(q, torch.Tensor) or q.dtype not in _DT:
             raise ValueError("q must be a bfloat16 or float16 tensor")
-        T = q.shape[0]
+        self._check_current()
+        T = q.shape[0] if q.dim() else 0
         qs = self._tokens("q", q, T, None, q.dtype)
         hq, D = q.shape[1], self.head_dim
         batch = self._batch_desc(cu_new, seq_lens, page_table)
-        _check_device(q, cache=self.k, cu_new=cu_new, seq_lens=seq_lens, page_table=page_table)
         if max_seq_len is None:
-            max_seq_len = page_table.shape[1] * self.page_size
+            max_seq_len = batch.table_width * self.page_size
         if out is None:
             out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
         else:
@@ -420,20 +461,28 @@ class KVCache:
             _check_output("lse", lse, T * hq * 4, q.device, torch.float32)
         elif return_lse:
             lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
-        cache = self._cache_desc()
-        need = ctypes.c_int64(0)
-        _lib.check(self._lib.fq_kv_attention_workspace(ctypes.byref(cache), ctypes.byref(batch), T, hq, int(max_q_len),
-                                                       int(max_seq_len), ctypes.byref(need)),
-                   "fq_kv_attention_workspace")
+        sizes = (T, hq, batch.num_seqs, batch.table_width, max_q_len, max_seq_len)
+        need = self._workspace_bytes.get(sizes)
+        if need is None:
+            n = ctypes.c_int64(0)
+            _lib.check(self._lib.fq_kv_attention_workspace(ctypes.byref(self._desc), ctypes.byref(batch), T, hq,
+                                                           int(max_q_len), int(max_seq_len), ctypes.byref(n)),
+                       "fq_kv_attention_workspace")
+            if len(self._workspace_bytes) >= 4096:
+                self._workspace_bytes.clear()
+            need = self._workspace_bytes[sizes] = n.value
         ws = None
-        if need.value:
-            ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
             if stream is not None:
                 ws.record_stream(stream)  # freed on this stream's clock, used on the other's
-        _lib.check(self._lib.fq_kv_attention(
-            ctypes.byref(cache), ctypes.byref(batch), T, _DT[q.dtype], _ptr(q), qs, hq, int(max_q_len),
-            int(max_seq_len), float(scale if scale is not None else D ** -0.5), int(bool(causal)), _ptr(out), _ptr(lse),
-            _ptr(ws), need.value, _ptr(self._status), _stream_ptr(stream)), "fq_kv_attention")
+        st = self._lib.fq_kv_attention(
+            ctypes.byref(self._desc), ctypes.byref(batch), T, _DT[q.dtype], q.data_ptr(), qs, hq, int(max_q_len),
+            int(max_seq_len), float(scale if scale is not None else D ** -0.5), 1 if causal else 0, out.data_ptr(),
+            lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None, need,
+            self._status_ptr, _raw_stream(stream, self._device))
+        if st != _lib.FQ_OK:
+            _lib.check(st, "fq_kv_attention")
         return (out, lse) if return_lse else out
 
 

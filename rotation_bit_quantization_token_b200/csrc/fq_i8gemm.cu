@@ -311,7 +311,8 @@ cudaError_t launch_t(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
   while (split < 8 && p.num_tiles * split * 2 <= num_sms * G::kMinBlocks && p.nk >= split * 2 * 4) split *= 2;
   p.split = split;
   auto kern = i8gemm_kernel<kBT, Out>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(kern), G::kSmem);
   if (e != cudaSuccess) return e;
   const int resident = num_sms * G::kMinBlocks;
   cudaLaunchConfig_t cfg{};
@@ -325,7 +326,7 @@ cudaError_t launch_t(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = split > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, map_w, map_a, p);
 }
 

@@ -329,7 +329,8 @@ cudaError_t launch_steps(const KvAppendParams& p0, int num_sms, cudaStream_t str
   groups = (p.c.kv_heads + p.heads_per_cta - 1) / p.heads_per_cta;
   const int smem = p.c.page_size * (p.rot_dim / 2) * int(sizeof(float2));
   auto kern = kv_append_kernel<T, D, kSteps>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = ptx::allow_smem(done, reinterpret_cast<const void*>(kern), 128 * (D / 2) * int(sizeof(float2)));
   if (e != cudaSuccess) return e;
   const int64_t q_tasks = p.q != nullptr ? p.T * ((p.q_heads + kQHeads - 1) / kQHeads) : 0;
   const int64_t kv_ctas = items * groups, ctas = kv_ctas + (q_tasks + kWarps - 1) / kWarps;

@@ -38,6 +38,7 @@ using namespace ptx;
 using namespace kv;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kMaxChunkBytes = 4096 * 128;  // of K in one chunk (V as much again)
 
 enum : uint32_t { kStFull = 1u << 0 };
 
@@ -576,7 +577,9 @@ cudaError_t launch_rows(const KvAttnParams& p, const KvAttnPlan& plan, cudaStrea
     return cudaErrorInvalidValue;
   const int pages = p.chunk / p.c.page_size + 1;
   const int smem = G_::kRing + int(sizeof(Shared)) + pages * 6 + 16 + 1024;
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const int most = G_::kRing + int(sizeof(Shared)) + (kMaxChunkBytes / D / 16 + 1) * 6 + 16 + 1024;
+  const cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(kv_attn_kernel<D, NT>), most);
   if (e != cudaSuccess) return e;
   const int64_t grid = int64_t(plan.row_tiles) * p.c.kv_heads * plan.splits * p.b.num_seqs;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
@@ -639,7 +642,7 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
     // the machine filled once (three CTAs on an SM), or chunks of 1 MB, whichever is smaller: a
     // ragged batch then ends evenly (64 sequences of 500-16000: 197 us with chunks of 2 MB, 182 with
     // 1 MB), and a CTA's start and end (about 3 us) and the join stay small beside its chunk
-    plan.chunk = int(chunk_for(max_seq_len, ctas, 3 * int64_t(num_sms), 256, 4096 * 128 / c.head_dim));
+    plan.chunk = int(chunk_for(max_seq_len, ctas, 3 * int64_t(num_sms), 256, kMaxChunkBytes / c.head_dim));
     plan.splits = int((max_seq_len + plan.chunk - 1) / plan.chunk);
   }
   if (rows > plan.tc_rows) {

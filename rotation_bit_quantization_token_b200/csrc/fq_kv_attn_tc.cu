@@ -706,11 +706,13 @@ cudaError_t launch_tc(const KvAttnParams& p, const KvAttnPlan& plan, cudaStream_
     return cudaErrorInvalidValue;
   auto kern = kv_attn_tc_kernel<D, kF16>;
   // setmaxnreg.inc draws on what the block was launched with
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
+  static const int regs = [&] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs != kRegsLaunch) return cudaErrorInvalidKernelImage;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(kern), Geo<D>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t grid = int64_t(plan.tc_row_tiles) * p.c.kv_heads * plan.tc_splits * p.b.num_seqs;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
