@@ -16,6 +16,10 @@
 // epilogue of one tile runs under the MMAs of the next. A lane holds one channel, so a
 // warp's stores of one token are 32 neighbouring outputs.
 // Roles, 256 threads: warp 0 TMA producer, warp 1 MMA issuer (owns TMEM), warps 4-7 epilogue.
+// Large products take i8gemm_pair_kernel: pairs of CTAs share 256 x 256 tiles (cta_group::2), each
+// loading 128 rows of both operands, 32 KB a stage instead of 48 for the same products. The single
+// kernel runs at 757 clocks a stage there (63 bytes a clock and SM, what L2 delivers), where the
+// MMAs need 512.
 // Every wait is bounded; on expiry the kernel sets a bit in the caller's status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,11 +47,13 @@ struct Geo {
   static constexpr int kABytes = kBT * kBK;
   static constexpr int kStage = kWBytes + kABytes;
   // two CTAs per SM for the narrow tiles (about 100 KB each in flight), one for the wide ones
-  static constexpr int kStages = kBT <= 16 ? 5 : (kBT <= 64 ? 4 : (kBT == 128 ? 6 : 4));
+  static constexpr int kStages = kBT <= 16 ? 5 : (kBT <= 64 ? 4 : (kBT == 128 ? 5 : 4));
   static constexpr int kMinBlocks = kBT <= 64 ? 2 : 1;
   static constexpr int kBufs = 2;
   static constexpr uint32_t kCols = kBufs * kBT < 32 ? 32u : uint32_t(kBufs * kBT);
-  static constexpr int kSmem = kStages * kStage + 1024 /*alignment*/ + 512 /*barriers*/;
+  // 32 outputs of up to 32 tokens for each epilogue warp (wide tiles only)
+  static constexpr int kStaging = kBT >= 128 ? 4 * 32 * 32 * 4 : 0;
+  static constexpr int kSmem = kStages * kStage + kStaging + 1024 /*alignment*/ + 512 /*barriers*/;
   static_assert(kSmem <= 227 * 1024 && kCols <= 512, "resources");
   static_assert(kBT * kBO * 4 <= kStages * kStage, "partial sums fit the ring");
 };
@@ -66,6 +72,7 @@ struct Params {
   uint32_t* status;
   int64_t T, O;
   int tiles_o, num_tiles, nk, split;
+  int vec;  // rows of C are 16-byte aligned
 };
 
 template <typename Out>
@@ -94,12 +101,52 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ int ld_remote(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ uint32_t remote_addr(uint32_t saddr, uint32_t rank) {
   uint32_t ra;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ra) : "memory");
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(saddr), "r"(rank));
+  return ra;
+}
+__device__ __forceinline__ int4 ld_remote4(uint32_t ra) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ra));
   return v;
+}
+
+// Scales and stores kChunk tokens (columns col .. of TMEM row t_col) of a warp's 32 channels. With
+// `stage` (this warp's shared memory, kChunk * 32 outputs) the tokens' 32 outputs leave as 16-byte
+// pieces; without it, or where the rows of C are not 16-byte aligned, one output per lane and store.
+template <int kChunk, typename Out>
+__device__ __forceinline__ void store_chunk(uint32_t t_col, const Params& p, int64_t t0, int64_t o0, float ws, int lane,
+                                            uint8_t* stage, bool vec) {
+  uint32_t r[kChunk];
+  if constexpr (kChunk == 16) tmem_ld16(t_col, r);
+  else tmem_ld32(t_col, r);
+  const float as = (lane < kChunk && t0 + lane < p.T) ? __ldg(p.a_scale + t0 + lane) : 0.0f;
+  tmem_wait_ld();
+  const int n = int(min(p.T - t0, int64_t(kChunk)));  // tokens there (may be negative)
+  Out y[kChunk];
+#pragma unroll
+  for (int e = 0; e < kChunk; ++e) y[e] = to_out<Out>(float(int(r[e])) * __shfl_sync(0xffffffffu, as, e) * ws);
+  if (vec && stage != nullptr && o0 + 32 <= p.O) {
+    Out* mine = reinterpret_cast<Out*>(stage);
+    __syncwarp();  // the last chunk has been read
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) mine[e * 32 + lane] = y[e];
+    __syncwarp();
+    constexpr int kPieces = 32 * int(sizeof(Out)) / 16, kPer = 32 / kPieces;  // pieces of a token, tokens per store
+    const int piece = lane % kPieces;
+#pragma unroll
+    for (int e = 0; e < kChunk; e += kPer) {
+      const int t = e + lane / kPieces;
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + t * 32 * int(sizeof(Out)) + piece * 16);
+      if (t < n) *(reinterpret_cast<uint4*>(static_cast<Out*>(p.C) + (t0 + t) * p.O + o0) + piece) = v;
+    }
+  } else if (o0 + lane < p.O) {
+    Out* dst = static_cast<Out*>(p.C) + t0 * p.O + o0 + lane;
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e, dst += p.O)
+      if (e < n) *dst = y[e];
+  }
 }
 
 template <int kBT, typename Out>
@@ -108,11 +155,27 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   using G = Geo<kBT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Bars* bars = reinterpret_cast<Bars*>(smem + G::kStages * G::kStage);
+  Bars* bars = reinterpret_cast<Bars*>(smem + G::kStages * G::kStage + G::kStaging);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr uint32_t kIdesc = (2u << 4) | (1u << 7) | (1u << 10) |  // int32 sums of signed bytes
                               (uint32_t(kBT >> 3) << 17) | (uint32_t(kBO >> 4) << 24);
+
+  // split = 1: tiles blockIdx.x, + gridDim.x, ...; split > 1: one tile per cluster, the
+  // cluster's CTA r taking the K stages [r nk / split, (r + 1) nk / split)
+  const int rank = p.split > 1 ? int(cluster_rank()) : 0;
+  const int first = p.split > 1 ? int(blockIdx.x) / p.split : int(blockIdx.x);
+  const int step = p.split > 1 ? p.num_tiles : int(gridDim.x);
+  const int n_local = first < p.num_tiles ? (p.num_tiles - 1 - first) / step + 1 : 0;
+  const int k0 = int(int64_t(p.nk) * rank / p.split), k1 = int(int64_t(p.nk) * (rank + 1) / p.split);
+  auto load = [&](int tile, int kb, int s) {
+    mbar_arrive_expect_tx(&bars->full[s], G::kStage);
+    const uint32_t dst = sbase + s * G::kStage;
+    tma_load_2d(dst, &map_w, kb * kBK, (tile % p.tiles_o) * kBO, &bars->full[s]);
+    tma_load_2d(dst + G::kWBytes, &map_a, kb * kBK, (tile / p.tiles_o) * kBT, &bars->full[s]);
+  };
+  // the first round of loads goes out before the CTA has met: nothing else writes the ring
+  const int n_early = n_local > 0 ? min(k1 - k0, G::kStages) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < G::kStages; ++s) {
@@ -125,6 +188,8 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     }
     bars->abort = 0;
     fence_barrier_init();
+    fence_proxy_async();
+    for (int s = 0; s < n_early; ++s) load(first, k0 + s, s);
   }
   if (warp == kWarpMma) tmem_alloc(&bars->tmem_base, G::kCols);
   tc_fence_before();
@@ -132,32 +197,19 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  // split = 1: tiles blockIdx.x, + gridDim.x, ...; split > 1: one tile per cluster, the
-  // cluster's CTA r taking the K stages [r nk / split, (r + 1) nk / split)
-  const int rank = p.split > 1 ? int(cluster_rank()) : 0;
-  const int first = p.split > 1 ? int(blockIdx.x) / p.split : int(blockIdx.x);
-  const int step = p.split > 1 ? p.num_tiles : int(gridDim.x);
-  const int n_local = first < p.num_tiles ? (p.num_tiles - 1 - first) / step + 1 : 0;
-  const int k0 = int(int64_t(p.nk) * rank / p.split), k1 = int(int64_t(p.nk) * (rank + 1) / p.split);
-
   if (warp == kWarpProducer) {
     if (lane == 0) {
-      int it = 0;
+      int it = n_early;
       bool ok = true;
       for (int i = 0; ok && i < n_local; ++i) {
-        const int tile = first + i * step;
-        const int o0 = (tile % p.tiles_o) * kBO, t0 = (tile / p.tiles_o) * kBT;
-        for (int kb = k0; kb < k1; ++kb, ++it) {
+        for (int kb = k0 + (i == 0 ? n_early : 0); kb < k1; ++kb, ++it) {
           const int s = it % G::kStages;
           if (it >= G::kStages &&
               !wait_bounded(&bars->empty[s], ((it / G::kStages) - 1) & 1, &bars->abort, p.status, kStEmpty)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&bars->full[s], G::kStage);
-          const uint32_t dst = sbase + s * G::kStage;
-          tma_load_2d(dst, &map_w, kb * kBK, o0, &bars->full[s]);
-          tma_load_2d(dst + G::kWBytes, &map_a, kb * kBK, t0, &bars->full[s]);
+          load(first + i * step, kb, s);
         }
       }
       // every issued load has landed before the CTA may exit (or reuse the ring)
@@ -231,27 +283,23 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       if (ok) {
         tc_fence_after();
         const float ws = o < p.O ? __ldg(p.w_scale + o) : 0.0f;
+        const int64_t o0 = int64_t(tile % p.tiles_o) * kBO + q * 32;
+        uint8_t* stage = G::kStaging > 0 ? smem + G::kStages * G::kStage + q * (G::kStaging / 4) : nullptr;
 #pragma unroll 1
         for (int c = 0; c < kBT / kChunk; ++c) {
-          uint32_t r[kChunk];
-          if constexpr (kChunk == 16) tmem_ld16(t_lane + uint32_t(buf * kBT + c * kChunk), r);
-          else tmem_ld32(t_lane + uint32_t(buf * kBT + c * kChunk), r);
-          const int64_t ts = t0 + c * kChunk + lane;
-          const float as = (lane < kChunk && ts < p.T) ? __ldg(p.a_scale + ts) : 0.0f;
-          tmem_wait_ld();
+          const uint32_t t_col = t_lane + uint32_t(buf * kBT + c * kChunk);
           if (p.split > 1) {
             // this CTA's partial sums, [token][channel], into its own (drained) ring: every
             // load of it has been read by an MMA that completed before d_full
+            uint32_t r[kChunk];
+            if constexpr (kChunk == 16) tmem_ld16(t_col, r);
+            else tmem_ld32(t_col, r);
+            tmem_wait_ld();
             int* part = reinterpret_cast<int*>(smem) + (c * kChunk) * kBO + q * 32 + lane;
 #pragma unroll
             for (int e = 0; e < kChunk; ++e) part[e * kBO] = int(r[e]);
-          } else {
-            Out* dst = static_cast<Out*>(p.C) + (t0 + c * kChunk) * p.O + o;
-#pragma unroll
-            for (int e = 0; e < kChunk; ++e) {
-              const float f = float(int(r[e])) * __shfl_sync(0xffffffffu, as, e) * ws;
-              if (t0 + c * kChunk + e < p.T && o < p.O) dst[int64_t(e) * p.O] = to_out<Out>(f);
-            }
+          } else if (t0 + c * kChunk < p.T) {
+            store_chunk<kChunk, Out>(t_col, p, t0 + c * kChunk, o0, ws, lane, stage, p.vec != 0);
           }
         }
       }
@@ -268,16 +316,38 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     cluster_sync();
     const bool good = *reinterpret_cast<volatile int*>(&bars->abort) == 0;
     const int per = (kBT + p.split - 1) / p.split;
-    const int64_t o = int64_t(first % p.tiles_o) * kBO + (threadIdx.x & (kBO - 1));
+    const int c4 = (threadIdx.x & 31) * 4;  // four channels of a token per thread, a warp per token
+    const int64_t o = int64_t(first % p.tiles_o) * kBO + c4;
     const int64_t t0 = int64_t(first / p.tiles_o) * kBT;
-    const float ws = o < p.O ? __ldg(p.w_scale + o) : 0.0f;
-    for (int e = rank * per + int(threadIdx.x) / kBO; good && e < min(kBT, (rank + 1) * per); e += kThreads / kBO) {
-      if (t0 + e >= p.T) break;
-      const uint32_t at = sbase + uint32_t(e * kBO + (threadIdx.x & (kBO - 1))) * 4u;
-      int sum = 0;
-      for (int r = 0; r < p.split; ++r) sum += ld_remote(at, uint32_t(r));
-      const float f = float(sum) * __ldg(p.a_scale + t0 + e) * ws;
-      if (o < p.O) static_cast<Out*>(p.C)[(t0 + e) * p.O + o] = to_out<Out>(f);
+    float ws[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) ws[k] = o + k < p.O ? __ldg(p.w_scale + o + k) : 0.0f;
+    const bool vec = o + 4 <= p.O && (p.O & 3) == 0 && (reinterpret_cast<uintptr_t>(p.C) & 15u) == 0;
+    const int e1 = min(min(kBT, (rank + 1) * per), int(min(p.T - t0, int64_t(kBT))));
+    const uint32_t mine = sbase + uint32_t(c4) * 4u;
+#pragma unroll 4
+    for (int e = rank * per + warp; e < e1; e += kThreads / 32) {
+      if (!good) break;
+      int4 sum = make_int4(0, 0, 0, 0);
+      for (int r = 0; r < p.split; ++r) {
+        const int4 v = ld_remote4(remote_addr(mine + uint32_t(e * kBO) * 4u, uint32_t(r)));
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+      }
+      const float as = __ldg(p.a_scale + t0 + e);
+      Out y[4] = {to_out<Out>(float(sum.x) * as * ws[0]), to_out<Out>(float(sum.y) * as * ws[1]),
+                  to_out<Out>(float(sum.z) * as * ws[2]), to_out<Out>(float(sum.w) * as * ws[3])};
+      Out* dst = static_cast<Out*>(p.C) + (t0 + e) * p.O + o;
+      if (vec) {
+        if constexpr (sizeof(Out) == 4) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(y);
+        else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(y);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (o + k < p.O) dst[k] = y[k];
+      }
     }
     cluster_sync();  // no CTA leaves while another reads its partial sums
   }
@@ -289,13 +359,8 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   }
 }
 
-template <int kBT, typename Out>
-cudaError_t launch_t(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
-  using G = Geo<kBT>;
-  CUtensorMap map_w, map_a;
-  if (!encode_bytes_2d(&map_w, g.w, uint64_t(g.O), uint64_t(g.L), kBK, kBO) ||
-      !encode_bytes_2d(&map_a, g.a, uint64_t(g.T), uint64_t(g.L), kBK, kBT))
-    return cudaErrorInvalidValue;
+template <typename Out>
+Params params_of(const I8GemmParams& g) {
   Params p{};
   p.a_scale = g.a_scale;
   p.w_scale = g.w_scale;
@@ -303,9 +368,224 @@ cudaError_t launch_t(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
   p.status = g.status;
   p.T = g.T;
   p.O = g.O;
+  p.nk = int((g.L + kBK - 1) / kBK);
+  p.vec = (reinterpret_cast<uintptr_t>(g.C) & 15u) == 0 && (g.O * int64_t(sizeof(Out))) % 16 == 0;
+  return p;
+}
+
+// ---- pairs of CTAs ----
+constexpr int kPairStages = 6, kPairStage = 2 * kBO * kBK;  // 128 rows of W and of A per CTA
+constexpr int kPairT = 256, kPairO = 256;
+constexpr int kPairStaging = 4 * 32 * 32 * 4;
+constexpr int kPairSmem = kPairStages * kPairStage + kPairStaging + 1024 + 512;
+static_assert(kPairSmem <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// arrives at the barrier's place in both CTAs of the pair
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(uint16_t(3))
+      : "memory");
+}
+
+template <typename Out>
+__global__ void __launch_bounds__(kThreads, 1)
+i8gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + kPairStages * kPairStage + kPairStaging);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  constexpr uint32_t kIdesc = (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kPairT >> 3) << 17) | (uint32_t(kPairO >> 4) << 24);
+  const int first = int(blockIdx.x) / 2, step = int(gridDim.x) / 2;
+  const int n_local = first < p.num_tiles ? (p.num_tiles - 1 - first) / step + 1 : 0;
+
+  // full and d_empty are the first CTA's (it issues the MMAs); empty and d_full are told to both
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->d_full[b], 1);
+      mbar_init(&bars->d_empty[b], 8);
+    }
+    bars->abort = 0;
+    fence_barrier_init();
+    fence_proxy_async();
+  }
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are there
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp == kWarpProducer) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < n_local; ++i) {
+        const int tile = first + i * step;
+        const int o0 = (tile % p.tiles_o) * kPairO + int(rank) * kBO, t0 = (tile / p.tiles_o) * kPairT + int(rank) * kBO;
+        for (int kb = 0; kb < p.nk; ++kb, ++it) {
+          const int s = it % kPairStages;
+          if (it >= kPairStages &&
+              !wait_bounded(&bars->empty[s], ((it / kPairStages) - 1) & 1, &bars->abort, p.status, kStEmpty)) {
+            ok = false;
+            break;
+          }
+          // the first CTA's barrier counts the bytes of both
+          if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2 * kPairStage);
+          const uint32_t bar = remote_addr(smem_u32(&bars->full[s]), 0);
+          const uint32_t dst = sbase + s * kPairStage;
+          tma_load_pair(dst, &map_w, kb * kBK, o0, bar);
+          tma_load_pair(dst + kPairStage / 2, &map_a, kb * kBK, t0, bar);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma && rank == 0) {
+    const bool leader = elect_one();
+    int it = 0;
+    bool ok = true;
+    for (int i = 0; ok && i < n_local; ++i) {
+      const int buf = i & 1;
+      if (i >= 2 && !warp_wait(&bars->d_empty[buf], ((i >> 1) - 1) & 1, &bars->abort, p.status, kStDEmpty)) break;
+      tc_fence_after();
+      for (int kb = 0; kb < p.nk; ++kb, ++it) {
+        const int s = it % kPairStages;
+        if (!warp_wait(&bars->full[s], (it / kPairStages) & 1, &bars->abort, p.status, kStFull)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (leader) {
+          const uint64_t wd = sw128_desc(sbase + s * kPairStage), ad = sw128_desc(sbase + s * kPairStage + kPairStage / 2);
+#pragma unroll
+          for (int k = 0; k < kBK / 32; ++k)
+            mma_i8_pair(tmem + uint32_t(buf * kPairT), wd + uint64_t((k * 32) >> 4), ad + uint64_t((k * 32) >> 4), kIdesc,
+                        (kb > 0 || k > 0) ? 1u : 0u);
+          commit_pair(&bars->empty[s]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (leader) commit_pair(&bars->d_full[buf]);
+      __syncwarp();
+    }
+    // every MMA issued here has completed before TMEM is released: the last commit of each stage
+    if (lane == 0) {
+      for (int j = it > kPairStages ? it - kPairStages : 0; j < it; ++j) {
+        const uint32_t b = smem_u32(&bars->empty[j % kPairStages]);
+        const uint64_t tz = globaltimer();
+        while (!mbar_try_wait(b, (j / kPairStages) & 1)) {
+          if (globaltimer() - tz > kTimeoutNs) {
+            if (p.status != nullptr) atomicOr(p.status, kStDrain);
+            break;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kWarpEpi0) {
+    const int q = warp - kWarpEpi0;
+    const uint32_t t_lane = tmem + (uint32_t(q * 32) << 16);
+    uint8_t* stage = smem + kPairStages * kPairStage + q * (kPairStaging / 4);
+    for (int i = 0; i < n_local; ++i) {
+      const int tile = first + i * step;
+      const int buf = i & 1;
+      const int64_t o0 = int64_t(tile % p.tiles_o) * kPairO + int64_t(rank) * kBO + q * 32;
+      const int64_t t0 = int64_t(tile / p.tiles_o) * kPairT;
+      const bool ok = warp_wait(&bars->d_full[buf], (i >> 1) & 1, &bars->abort, p.status, kStDFull);
+      if (ok) {
+        tc_fence_after();
+        const float ws = o0 + lane < p.O ? __ldg(p.w_scale + o0 + lane) : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < kPairT / 32; ++c)
+          if (t0 + c * 32 < p.T)
+            store_chunk<32, Out>(t_lane + uint32_t(buf * kPairT + c * 32), p, t0 + c * 32, o0, ws, lane, stage, p.vec != 0);
+      }
+      // the accumulator is free for the tile after next
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t bar = remote_addr(smem_u32(&bars->d_empty[buf]), 0);
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+      }
+      if (!ok) break;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither leaves while the other's MMAs or arrivals may reach it
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+template <typename Out>
+cudaError_t launch_pair(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
+  CUtensorMap map_w, map_a;
+  if (!encode_bytes_2d(&map_w, g.w, uint64_t(g.O), uint64_t(g.L), kBK, kBO) ||
+      !encode_bytes_2d(&map_a, g.a, uint64_t(g.T), uint64_t(g.L), kBK, kBO))
+    return cudaErrorInvalidValue;
+  Params p = params_of<Out>(g);
+  p.tiles_o = int((g.O + kPairO - 1) / kPairO);
+  p.num_tiles = p.tiles_o * int((g.T + kPairT - 1) / kPairT);
+  p.split = 1;
+  auto kern = i8gemm_pair_kernel<Out>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(kern), kPairSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = p.num_tiles < num_sms / 2 ? p.num_tiles : num_sms / 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, map_w, map_a, p);
+}
+
+template <int kBT, typename Out>
+cudaError_t launch_t(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
+  using G = Geo<kBT>;
+  CUtensorMap map_w, map_a;
+  if (!encode_bytes_2d(&map_w, g.w, uint64_t(g.O), uint64_t(g.L), kBK, kBO) ||
+      !encode_bytes_2d(&map_a, g.a, uint64_t(g.T), uint64_t(g.L), kBK, kBT))
+    return cudaErrorInvalidValue;
+  Params p = params_of<Out>(g);
   p.tiles_o = int((g.O + kBO - 1) / kBO);
   p.num_tiles = p.tiles_o * int((g.T + kBT - 1) / kBT);
-  p.nk = int((g.L + kBK - 1) / kBK);
   // split K until every SM has its CTAs, as long as each CTA keeps four stages of work
   int split = 1;
   while (split < 8 && p.num_tiles * split * 2 <= num_sms * G::kMinBlocks && p.nk >= split * 2 * 4) split *= 2;
@@ -336,6 +616,9 @@ cudaError_t launch_out(const I8GemmParams& g, int num_sms, cudaStream_t stream) 
   if (g.T <= 32) return launch_t<32, Out>(g, num_sms, stream);
   if (g.T <= 64) return launch_t<64, Out>(g, num_sms, stream);
   if (g.T <= 128) return launch_t<128, Out>(g, num_sms, stream);
+  // pairs where their tiles come close to filling the machine
+  const int64_t pairs = ((g.O + kPairO - 1) / kPairO) * ((g.T + kPairT - 1) / kPairT);
+  if (pairs * 10 >= int64_t(num_sms / 2) * 7) return launch_pair<Out>(g, num_sms, stream);
   return launch_t<256, Out>(g, num_sms, stream);
 }
 

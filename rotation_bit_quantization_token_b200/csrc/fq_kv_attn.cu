@@ -497,6 +497,7 @@ kv_attn_join_kernel(const KvAttnParams p) {
   constexpr int kCols = D / 4, kGroups = kThreads / kCols;
   const int tid = threadIdx.x;
   const int col = tid % kCols, grp = tid / kCols;
+  grid_dependency_wait();  // every thread, so that this kernel never ends before the attention does
   const int64_t row = kWide ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * kGroups + grp;
   if (row >= p.T * p.q_heads) return;
   const int64_t t = row / p.q_heads;
@@ -516,7 +517,6 @@ kv_attn_join_kernel(const KvAttnParams p) {
   if (i < 0 || i >= s.n || i >= p.max_q_len || s.end <= chunk) return;
   const int n = int((s.end + chunk - 1) / chunk);
   const float* src = p.ws + row * p.ws_splits * (D + 4);
-  grid_dependency_wait();  // the chunks' results
   // a running maximum, as in the chunks themselves
   float M = -INFINITY, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

@@ -44,7 +44,9 @@ def _dev(*arrays):
 # every token-tile width and its neighbours, ragged channels, K down to 16 codes, K tails of 16
 SHAPES = [(1, 1, 16), (1, 128, 4096), (3, 130, 144), (16, 300, 2048), (17, 64, 4112), (32, 1000, 1024),
           (33, 257, 2064), (64, 129, 8192), (65, 384, 512), (128, 255, 1040), (129, 640, 4096), (300, 1030, 1552),
-          (777, 513, 2048), (2, 5000, 16384), (1000, 3, 96)]
+          (777, 513, 2048), (2, 5000, 16384), (1000, 3, 96),
+          # pairs of CTAs: one tile each, several each (aligned and unaligned rows of C), long K
+          (1990, 2100, 272), (300, 8200, 512), (2600, 3001, 144), (2600, 3008, 400), (2049, 2056, 4096)]
 
 
 @pytest.mark.parametrize("T,O,L", SHAPES)
