@@ -10,8 +10,8 @@
 // Layout of the work: the weights' rows lie on the TMEM lanes (M = 128 channels), tokens
 // along the MMA's N (kBT = 16 .. 256), K in stages of 128 codes (one 128-byte swizzle atom).
 // With few tokens the product is bound by reading the weights once, so the tile has no more
-// token columns than needed, and the CTAs of a cluster split K between them and add their
-// int32 partial sums through distributed shared memory (exact, whatever the order). With
+// token columns than needed, and the CTAs of a cluster split K between them and send their int32
+// partial sums to the one that owns the token (exact, whatever the order). With
 // many tokens each CTA walks over tiles and the accumulator is double buffered, so that the
 // epilogue of one tile runs under the MMAs of the next. A lane holds one channel, so a
 // warp's stores of one token are 32 neighbouring outputs.
@@ -39,28 +39,36 @@ constexpr int kBK = 128;       // codes per row and stage
 constexpr int kThreads = 256;
 constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi0 = 4;
 
-enum : uint32_t { kStFull = 1u << 0, kStEmpty = 1u << 1, kStDFull = 1u << 2, kStDEmpty = 1u << 3, kStDrain = 1u << 4 };
+enum : uint32_t { kStFull = 1u << 0, kStEmpty = 1u << 1, kStDFull = 1u << 2, kStDEmpty = 1u << 3, kStDrain = 1u << 4, kStIn = 1u << 5 };
 
-template <int kBT>
+// kSplit: the CTAs of a cluster share one tile's K
+template <int kBT, bool kSplit>
 struct Geo {
   static constexpr int kWBytes = kBO * kBK;
   static constexpr int kABytes = kBT * kBK;
   static constexpr int kStage = kWBytes + kABytes;
   // two CTAs per SM for the narrow tiles (about 100 KB each in flight), one for the wide ones
-  static constexpr int kStages = kBT <= 16 ? 5 : (kBT <= 64 ? 4 : (kBT == 128 ? 5 : 4));
   static constexpr int kMinBlocks = kBT <= 64 ? 2 : 1;
-  static constexpr int kBufs = 2;
+  static constexpr int kStages = kBT <= 16 ? 5 : (kBT <= 32 ? 4 : (kBT == 64 ? (kSplit ? 3 : 4) : (kBT == 128 ? (kSplit ? 4 : 5) : (kSplit ? 3 : 4))));
+  static constexpr int kMaxSplit = kBT == 256 ? 2 : (kBT == 64 ? 4 : 8);  // as the partial sums fit
+  static constexpr int kBufs = kSplit ? 1 : 2;  // accumulators
   static constexpr uint32_t kCols = kBufs * kBT < 32 ? 32u : uint32_t(kBufs * kBT);
+  // partial sums from the other CTAs of the cluster, [sender][channel][token of this CTA's share]; a
+  // channel's row is 16 bytes longer than its tokens, so that neighbouring lanes read other banks
+  static constexpr int in_bytes(int split) { return (split - 1) * kBO * (kBT / split + 4) * 4; }
+  static constexpr int kInBytes = kSplit ? in_bytes(kMaxSplit) : 0;  // grows with the split
   // 32 outputs of up to 32 tokens for each epilogue warp (wide tiles only)
-  static constexpr int kStaging = kBT >= 128 ? 4 * 32 * 32 * 4 : 0;
-  static constexpr int kSmem = kStages * kStage + kStaging + 1024 /*alignment*/ + 512 /*barriers*/;
-  static_assert(kSmem <= 227 * 1024 && kCols <= 512, "resources");
-  static_assert(kBT * kBO * 4 <= kStages * kStage, "partial sums fit the ring");
+  static constexpr int kStaging = kBT >= 128 && !kSplit ? 4 * 32 * 32 * 4 : 0;
+  static constexpr int kOffIn = kStages * kStage;
+  static constexpr int kOffBars = kOffIn + kInBytes + kStaging;
+  static constexpr int kSmem = kOffBars + 1024 /*alignment*/ + 512 /*barriers*/;
+  static_assert(kSmem * kMinBlocks <= (227 - (kMinBlocks - 1)) * 1024 && kCols <= 512, "resources");
 };
 
 struct Bars {
   uint64_t full[8], empty[8];
   uint64_t d_full[2], d_empty[2];
+  uint64_t in_full;  // the other CTAs' partial sums are there
   uint32_t tmem_base;
   int abort;
 };
@@ -106,10 +114,16 @@ __device__ __forceinline__ uint32_t remote_addr(uint32_t saddr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(saddr), "r"(rank));
   return ra;
 }
-__device__ __forceinline__ int4 ld_remote4(uint32_t ra) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ra));
-  return v;
+// Four (two) words to another CTA's shared memory, counted by its barrier.
+__device__ __forceinline__ void push4(uint32_t dst, const uint32_t* v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(dst),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void push2(uint32_t dst, const uint32_t* v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1,%2}, [%3];" ::"r"(dst), "r"(v[0]),
+               "r"(v[1]), "r"(bar)
+               : "memory");
 }
 
 // Scales and stores kChunk tokens (columns col .. of TMEM row t_col) of a warp's 32 channels. With
@@ -149,25 +163,26 @@ __device__ __forceinline__ void store_chunk(uint32_t t_col, const Params& p, int
   }
 }
 
-template <int kBT, typename Out>
-__global__ void __launch_bounds__(kThreads, Geo<kBT>::kMinBlocks)
+template <int kBT, typename Out, bool kSplit>
+__global__ void __launch_bounds__(kThreads, Geo<kBT, kSplit>::kMinBlocks)
 i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const Params p) {
-  using G = Geo<kBT>;
+  using G = Geo<kBT, kSplit>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Bars* bars = reinterpret_cast<Bars*>(smem + G::kStages * G::kStage + G::kStaging);
+  Bars* bars = reinterpret_cast<Bars*>(smem + G::kOffBars);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr uint32_t kIdesc = (2u << 4) | (1u << 7) | (1u << 10) |  // int32 sums of signed bytes
                               (uint32_t(kBT >> 3) << 17) | (uint32_t(kBO >> 4) << 24);
 
-  // split = 1: tiles blockIdx.x, + gridDim.x, ...; split > 1: one tile per cluster, the
-  // cluster's CTA r taking the K stages [r nk / split, (r + 1) nk / split)
-  const int rank = p.split > 1 ? int(cluster_rank()) : 0;
-  const int first = p.split > 1 ? int(blockIdx.x) / p.split : int(blockIdx.x);
-  const int step = p.split > 1 ? p.num_tiles : int(gridDim.x);
+  // not split: tiles blockIdx.x, + gridDim.x, ...; split: one tile per cluster, the cluster's CTA r
+  // taking the K stages [r nk / split, (r + 1) nk / split)
+  const int rank = kSplit ? int(cluster_rank()) : 0;
+  const int first = kSplit ? int(blockIdx.x) / p.split : int(blockIdx.x);
+  const int step = kSplit ? p.num_tiles : int(gridDim.x);
   const int n_local = first < p.num_tiles ? (p.num_tiles - 1 - first) / step + 1 : 0;
-  const int k0 = int(int64_t(p.nk) * rank / p.split), k1 = int(int64_t(p.nk) * (rank + 1) / p.split);
+  const int k0 = kSplit ? p.nk * rank / p.split : 0, k1 = kSplit ? p.nk * (rank + 1) / p.split : p.nk;
+  const int per = kSplit ? kBT / p.split : kBT;  // tokens of this CTA's share of the outputs
   auto load = [&](int tile, int kb, int s) {
     mbar_arrive_expect_tx(&bars->full[s], G::kStage);
     const uint32_t dst = sbase + s * G::kStage;
@@ -186,9 +201,11 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       mbar_init(&bars->d_full[b], 1);
       mbar_init(&bars->d_empty[b], 4);
     }
+    mbar_init(&bars->in_full, 1);
     bars->abort = 0;
     fence_barrier_init();
     fence_proxy_async();
+    if constexpr (kSplit) mbar_arrive_expect_tx(&bars->in_full, uint32_t((p.split - 1) * per * kBO * 4));
     for (int s = 0; s < n_early; ++s) load(first, k0 + s, s);
   }
   if (warp == kWarpMma) tmem_alloc(&bars->tmem_base, G::kCols);
@@ -196,7 +213,14 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  // the cluster meets before a partial sum is sent (its CTAs run and their barriers are there); the
+  // arrival is here, the wait just before sending, long after the others have arrived
+  if constexpr (kSplit) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
+  if constexpr (kSplit) {
+    // every warp of every CTA waits (the producer and issuer after their loops), so none may be left out
+    if (warp == 2 || warp == 3) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
   if (warp == kWarpProducer) {
     if (lane == 0) {
       int it = n_early;
@@ -284,24 +308,91 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         tc_fence_after();
         const float ws = o < p.O ? __ldg(p.w_scale + o) : 0.0f;
         const int64_t o0 = int64_t(tile % p.tiles_o) * kBO + q * 32;
-        uint8_t* stage = G::kStaging > 0 ? smem + G::kStages * G::kStage + q * (G::kStaging / 4) : nullptr;
+        uint8_t* stage = G::kStaging > 0 ? smem + G::kOffIn + q * (G::kStaging / 4) : nullptr;
+        if constexpr (kSplit) {
+          asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+          // Partial sums go to the CTA that owns the token, four tokens of a channel at a time (the sum
+          // of integers is exact in any order); then this CTA's own share is completed and stored. No
+          // CTA reads another's memory, so each may leave when it is done: two cluster barriers around
+          // remote reads took 4000 clocks more.
+          const int per_log = 31 - __clz(per);
+          const int ch = q * 32 + lane;
+          const uint32_t in_base = sbase + G::kOffIn, in_bar = smem_u32(&bars->in_full);
 #pragma unroll 1
-        for (int c = 0; c < kBT / kChunk; ++c) {
-          const uint32_t t_col = t_lane + uint32_t(buf * kBT + c * kChunk);
-          if (p.split > 1) {
-            // this CTA's partial sums, [token][channel], into its own (drained) ring: every
-            // load of it has been read by an MMA that completed before d_full
+          for (int c = 0; c < kBT / kChunk; ++c) {
+            if ((c * kChunk) >> per_log == rank && (c * kChunk + kChunk - 1) >> per_log == rank) continue;
             uint32_t r[kChunk];
+            const uint32_t t_col = t_lane + uint32_t(c * kChunk);
             if constexpr (kChunk == 16) tmem_ld16(t_col, r);
             else tmem_ld32(t_col, r);
             tmem_wait_ld();
-            int* part = reinterpret_cast<int*>(smem) + (c * kChunk) * kBO + q * 32 + lane;
+            if (per_log >= 2) {
 #pragma unroll
-            for (int e = 0; e < kChunk; ++e) part[e * kBO] = int(r[e]);
-          } else if (t0 + c * kChunk < p.T) {
-            store_chunk<kChunk, Out>(t_col, p, t0 + c * kChunk, o0, ws, lane, stage, p.vec != 0);
+              for (int e = 0; e < kChunk; e += 4) {
+                const int t = c * kChunk + e, dest = t >> per_log;
+                const int slot = rank - (rank > dest ? 1 : 0);
+                if (dest != rank)
+                  push4(remote_addr(in_base + uint32_t(((slot * kBO + ch) * (per + 4) + (t & (per - 1))) * 4), uint32_t(dest)), r + e,
+                        remote_addr(in_bar, uint32_t(dest)));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < kChunk; e += 2) {
+                const int dest = (c * kChunk + e) >> 1;
+                const int slot = rank - (rank > dest ? 1 : 0);
+                if (dest != rank)
+                  push2(remote_addr(in_base + uint32_t((slot * kBO + ch) * (per + 4) * 4), uint32_t(dest)), r + e,
+                        remote_addr(in_bar, uint32_t(dest)));
+              }
+            }
           }
+          if (!warp_wait(&bars->in_full, 0, &bars->abort, p.status, kStIn)) break;
+#pragma unroll 1
+          for (int c = rank * per / kChunk; c * kChunk < (rank + 1) * per; ++c) {
+            uint32_t r[kChunk];
+            const uint32_t t_col = t_lane + uint32_t(c * kChunk);
+            if constexpr (kChunk == 16) tmem_ld16(t_col, r);
+            else tmem_ld32(t_col, r);
+            const int64_t tc = t0 + c * kChunk;
+            const float as = (lane < kChunk && tc + lane < p.T) ? __ldg(p.a_scale + tc + lane) : 0.0f;
+            tmem_wait_ld();
+            for (int slot = 0; slot < p.split - 1; ++slot) {
+              const int* in = reinterpret_cast<const int*>(smem + G::kOffIn) + (slot * kBO + ch) * (per + 4) - rank * per;
+              if (per_log >= 2) {
+#pragma unroll
+                for (int e = 0; e < kChunk; e += 4) {
+                  if ((c * kChunk + e) >> per_log != rank) continue;
+                  const int4 v = *reinterpret_cast<const int4*>(in + c * kChunk + e);
+                  r[e] += uint32_t(v.x);
+                  r[e + 1] += uint32_t(v.y);
+                  r[e + 2] += uint32_t(v.z);
+                  r[e + 3] += uint32_t(v.w);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < kChunk; e += 2) {
+                  if ((c * kChunk + e) >> 1 != rank) continue;
+                  r[e] += uint32_t(in[c * kChunk + e]);
+                  r[e + 1] += uint32_t(in[c * kChunk + e + 1]);
+                }
+              }
+            }
+            const bool there = o < p.O;
+            Out* dst = static_cast<Out*>(p.C) + tc * p.O + o;
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e, dst += p.O) {
+              const float f = float(int(r[e])) * __shfl_sync(0xffffffffu, as, e) * ws;
+              if (there && (c * kChunk + e) >> per_log == rank && tc + e < p.T) *dst = to_out<Out>(f);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kBT / kChunk; ++c)
+            if (t0 + c * kChunk < p.T)
+              store_chunk<kChunk, Out>(t_lane + uint32_t(buf * kBT + c * kChunk), p, t0 + c * kChunk, o0, ws, lane, stage, p.vec != 0);
         }
+      } else if constexpr (kSplit) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       }
       // the accumulator is free for the tile after next
       tc_fence_before();
@@ -311,45 +402,8 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     }
   }
 
-  if (p.split > 1) {
-    // each CTA adds up its share of the tokens from all CTAs of the cluster
-    cluster_sync();
-    const bool good = *reinterpret_cast<volatile int*>(&bars->abort) == 0;
-    const int per = (kBT + p.split - 1) / p.split;
-    const int c4 = (threadIdx.x & 31) * 4;  // four channels of a token per thread, a warp per token
-    const int64_t o = int64_t(first % p.tiles_o) * kBO + c4;
-    const int64_t t0 = int64_t(first / p.tiles_o) * kBT;
-    float ws[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) ws[k] = o + k < p.O ? __ldg(p.w_scale + o + k) : 0.0f;
-    const bool vec = o + 4 <= p.O && (p.O & 3) == 0 && (reinterpret_cast<uintptr_t>(p.C) & 15u) == 0;
-    const int e1 = min(min(kBT, (rank + 1) * per), int(min(p.T - t0, int64_t(kBT))));
-    const uint32_t mine = sbase + uint32_t(c4) * 4u;
-#pragma unroll 4
-    for (int e = rank * per + warp; e < e1; e += kThreads / 32) {
-      if (!good) break;
-      int4 sum = make_int4(0, 0, 0, 0);
-      for (int r = 0; r < p.split; ++r) {
-        const int4 v = ld_remote4(remote_addr(mine + uint32_t(e * kBO) * 4u, uint32_t(r)));
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
-      }
-      const float as = __ldg(p.a_scale + t0 + e);
-      Out y[4] = {to_out<Out>(float(sum.x) * as * ws[0]), to_out<Out>(float(sum.y) * as * ws[1]),
-                  to_out<Out>(float(sum.z) * as * ws[2]), to_out<Out>(float(sum.w) * as * ws[3])};
-      Out* dst = static_cast<Out*>(p.C) + (t0 + e) * p.O + o;
-      if (vec) {
-        if constexpr (sizeof(Out) == 4) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(y);
-        else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(y);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (o + k < p.O) dst[k] = y[k];
-      }
-    }
-    cluster_sync();  // no CTA leaves while another reads its partial sums
+  if constexpr (kSplit) {
+    if (warp == kWarpProducer || warp == kWarpMma) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -576,9 +630,9 @@ cudaError_t launch_pair(const I8GemmParams& g, int num_sms, cudaStream_t stream)
   return cudaLaunchKernelEx(&cfg, kern, map_w, map_a, p);
 }
 
-template <int kBT, typename Out>
-cudaError_t launch_t(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
-  using G = Geo<kBT>;
+template <int kBT, typename Out, bool kSplit>
+cudaError_t launch_t(const I8GemmParams& g, int split, int num_sms, cudaStream_t stream) {
+  using G = Geo<kBT, kSplit>;
   CUtensorMap map_w, map_a;
   if (!encode_bytes_2d(&map_w, g.w, uint64_t(g.O), uint64_t(g.L), kBK, kBO) ||
       !encode_bytes_2d(&map_a, g.a, uint64_t(g.T), uint64_t(g.L), kBK, kBT))
@@ -586,17 +640,14 @@ cudaError_t launch_t(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
   Params p = params_of<Out>(g);
   p.tiles_o = int((g.O + kBO - 1) / kBO);
   p.num_tiles = p.tiles_o * int((g.T + kBT - 1) / kBT);
-  // split K until every SM has its CTAs, as long as each CTA keeps four stages of work
-  int split = 1;
-  while (split < 8 && p.num_tiles * split * 2 <= num_sms * G::kMinBlocks && p.nk >= split * 2 * 4) split *= 2;
   p.split = split;
-  auto kern = i8gemm_kernel<kBT, Out>;
+  auto kern = i8gemm_kernel<kBT, Out, kSplit>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(kern), G::kSmem);
+  const cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(kern), G::kSmem);
   if (e != cudaSuccess) return e;
   const int resident = num_sms * G::kMinBlocks;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(split > 1 ? p.num_tiles * split : (p.num_tiles < resident ? p.num_tiles : resident)));
+  cfg.gridDim = dim3(unsigned(kSplit ? p.num_tiles * split : (p.num_tiles < resident ? p.num_tiles : resident)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = G::kSmem;
   cfg.stream = stream;
@@ -606,20 +657,30 @@ cudaError_t launch_t(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = split > 1 ? 1 : 0;
+  cfg.numAttrs = kSplit ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, map_w, map_a, p);
+}
+
+template <int kBT, typename Out>
+cudaError_t launch_tile(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
+  using G = Geo<kBT, true>;
+  const int64_t tiles = ((g.O + kBO - 1) / kBO) * ((g.T + kBT - 1) / kBT), nk = (g.L + kBK - 1) / kBK;
+  // split K until every SM has its CTAs, as long as each CTA keeps four stages of work
+  int split = 1;
+  while (split < G::kMaxSplit && tiles * split * 2 <= num_sms * G::kMinBlocks && nk >= split * 2 * 4) split *= 2;
+  return split > 1 ? launch_t<kBT, Out, true>(g, split, num_sms, stream) : launch_t<kBT, Out, false>(g, 1, num_sms, stream);
 }
 
 template <typename Out>
 cudaError_t launch_out(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
-  if (g.T <= 16) return launch_t<16, Out>(g, num_sms, stream);
-  if (g.T <= 32) return launch_t<32, Out>(g, num_sms, stream);
-  if (g.T <= 64) return launch_t<64, Out>(g, num_sms, stream);
-  if (g.T <= 128) return launch_t<128, Out>(g, num_sms, stream);
+  if (g.T <= 16) return launch_tile<16, Out>(g, num_sms, stream);
+  if (g.T <= 32) return launch_tile<32, Out>(g, num_sms, stream);
+  if (g.T <= 64) return launch_tile<64, Out>(g, num_sms, stream);
+  if (g.T <= 128) return launch_tile<128, Out>(g, num_sms, stream);
   // pairs where their tiles come close to filling the machine
   const int64_t pairs = ((g.O + kPairO - 1) / kPairO) * ((g.T + kPairT - 1) / kPairT);
   if (pairs * 10 >= int64_t(num_sms / 2) * 7) return launch_pair<Out>(g, num_sms, stream);
-  return launch_t<256, Out>(g, num_sms, stream);
+  return launch_tile<256, Out>(g, num_sms, stream);
 }
 
 }  // namespace
