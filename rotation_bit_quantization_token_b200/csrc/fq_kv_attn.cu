@@ -135,6 +135,18 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   const int keys = int(min(int64_t(p.chunk), s.end - c0));
   const bool whole = s.end <= p.chunk;          // no other chunk: the result is final
 
+  // ---- q on its way: this thread's elements t4 * D/4 .. + D/4 of row g (and g + 8) ----
+  uint4 qw[NT][D / 32];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = row0 + g + 8 * n;
+    const bool live = g + 8 * n < rows;
+    const int64_t base = live ? (s.t_first + r / G) * p.q_stride + int64_t(h * G + r % G) * D + t4 * (D / 4) : 0;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      qw[n][c] = live ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + base) + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+
   // ---- page numbers of the chunk, barriers ----
   // scales beside them: (k exponent, v exponent) as bytes; a page outside the cache is -1
   int* s_page = reinterpret_cast<int*>(sh + 1);
@@ -193,7 +205,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     s_scale[i] = uint16_t((ke + 127) | ((ve + 127) << 8));
   }
 
-  // ---- q: this thread's elements t4 * D/4 .. + D/4 of row g (and g + 8) ----
+  // ---- q as fragments ----
   uint32_t qf[NT][kS][2];
   float rowf[NT][2];  // score factor of rows 2 t4, 2 t4 + 1 (+ 8)
   int vis[NT][2];     // keys of the chunk that they see
@@ -203,12 +215,9 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     const bool live = g + 8 * n < rows;
     float x[D / 4];
     float amax = 0.0f;
-    const int64_t base = live ? (s.t_first + r / G) * p.q_stride + int64_t(h * G + r % G) * D + t4 * (D / 4) : 0;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (live) w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + base) + c);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t ww[4] = {qw[n][c].x, qw[n][c].y, qw[n][c].z, qw[n][c].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 f = unpack16(ww[e], p.fp16);
@@ -493,28 +502,46 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 // has a row of its own (many rows with a few chunks).
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kThreads)
-kv_attn_join_kernel(const KvAttnParams p) {
+kv_attn_join_kernel(const KvAttnParams p, const int few) {
   constexpr int kCols = D / 4, kGroups = kThreads / kCols;
   const int tid = threadIdx.x;
   const int col = tid % kCols, grp = tid / kCols;
-  grid_dependency_wait();  // every thread, so that this kernel never ends before the attention does
-  const int64_t row = kWide ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * kGroups + grp;
-  if (row >= p.T * p.q_heads) return;
-  const int64_t t = row / p.q_heads;
-  const int hq = int(row - t * p.q_heads);
-  int lo = 0, hi = p.b.num_seqs - 1;  // the last sequence that starts at or before t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.b.cu_new + mid) <= t) lo = mid;
-    else hi = mid - 1;
-  }
+  int64_t row = kWide ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * kGroups + grp;
   const int G = p.q_heads / p.c.kv_heads;
+  int64_t t = 0;
+  int hq = 0, lo = 0;
+  bool live = true;
+  if (few > 0) {
+    // only sequences of at most `few` rows can have chunks: row r of head h of sequence b
+    const int64_t bh = row / few;
+    const int r = int(row - bh * few), h = int(bh % p.c.kv_heads);
+    live = bh / p.c.kv_heads < p.b.num_seqs;
+    lo = live ? int(bh / p.c.kv_heads) : 0;
+    hq = h * G + r % G;
+    t = int64_t(__ldg(p.b.cu_new + lo)) + r / G;
+    live = live && t >= 0 && t < p.T;
+    row = t * p.q_heads + hq;
+  } else {
+    live = row < p.T * p.q_heads;
+    t = row / p.q_heads;
+    hq = int(row - t * p.q_heads);
+    int hi = p.b.num_seqs - 1;  // the last sequence that starts at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(p.b.cu_new + mid) <= t) lo = mid;
+      else hi = mid - 1;
+    }
+  }
   const int64_t i = t - __ldg(p.b.cu_new + lo);
   const int64_t n_new = int64_t(__ldg(p.b.cu_new + lo + 1)) - __ldg(p.b.cu_new + lo);
   const bool tc = takes_tc(p, n_new, G);
   const int tile_rows = tc ? kTcRows : p.tile_rows, chunk = tc ? p.tc_chunk : p.chunk;
   const Rows s = sequence_rows(p, lo, (i * G + hq % G) / tile_rows * tile_rows, tile_rows, G);
-  if (i < 0 || i >= s.n || i >= p.max_q_len || s.end <= chunk) return;
+  live = live && i >= 0 && i < s.n && i < p.max_q_len && s.end > chunk;
+  // every thread waits, also where there is nothing to do: this kernel must not end before the
+  // attention does, or what comes after it could start beside that
+  grid_dependency_wait();
+  if (!live) return;
   const int n = int((s.end + chunk - 1) / chunk);
   const float* src = p.ws + row * p.ws_splits * (D + 4);
   // a running maximum, as in the chunks themselves
@@ -595,7 +622,9 @@ cudaError_t launch_attn(const KvAttnParams& p, const KvAttnPlan& plan, cudaStrea
   }
   if (p.ws_splits > 1) {
     // launched with the attention kernel still running (its blocks wait for it to complete)
-    const int64_t rows = p.T * p.q_heads;
+    // beside prompts that are not split, only the few rows of the other sequences can be
+    const int few = plan.tc_row_tiles > 0 && plan.tc_splits == 1 ? plan.row_tiles * plan.tile_rows : 0;
+    const int64_t rows = few > 0 ? int64_t(p.b.num_seqs) * p.c.kv_heads * few : p.T * p.q_heads;
     const bool wide = p.ws_splits > 8;
     const int64_t blocks = wide ? rows : (rows + kThreads / (D / 4) - 1) / (kThreads / (D / 4));
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
@@ -608,8 +637,8 @@ cudaError_t launch_attn(const KvAttnParams& p, const KvAttnPlan& plan, cudaStrea
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return wide ? cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<D, true>, p)
-                : cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<D, false>, p);
+    return wide ? cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<D, true>, p, few)
+                : cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<D, false>, p, few);
   }
   return cudaSuccess;
 }

@@ -36,6 +36,8 @@ using namespace kv;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kKeys = 128;  // keys of a step
+constexpr int kPFirst = 96; // keys whose probabilities are handed over first
+constexpr int kSorted = 256;  // sequences that are taken in order of length
 constexpr int kWarpConv0 = 8, kWarpProducer = 12, kWarpMma = 13;
 // Register split (setmaxnreg): launched at 128 per thread; 2 softmax warpgroups, the converters, the rest
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsConv = 72, kRegsLow = 40;
@@ -68,7 +70,7 @@ struct Bars {
   // unit u = 2j is K of step j, u = 2j + 1 V of step j
   uint64_t raw_full[4], raw_empty[4];  // codes of unit u, slot u % 4
   uint64_t t_full[3], t_empty[3];      // converted tile of unit u, slot u % 3
-  uint64_t s_full[2], p_full[2][2];  // row tile; P by halves of 64 keys
+  uint64_t s_full[2], p_full[2][2];  // row tile; P in two parts
   uint64_t o_full[2];                // row tile: O complete
   uint64_t q_full;
   uint64_t mma_done;
@@ -76,6 +78,7 @@ struct Bars {
   int abort;
   int k_top[kWarps], v_top[kWarps];  // largest page exponents of the CTA's keys, by warp
   int8_t q_exp[kTcRows];   // exponents of Q's rows
+  int sorted;
   // per step (mod 16; the producer is at most 4 + 3 steps ahead): the step's pages that are there, one
   // bit per 16 keys
   uint32_t valid[16];
@@ -117,20 +120,19 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b, u
         "l"(a), "l"(b), "r"(idesc)
         : "memory");
 }
-// O += P V for 64 keys: four K steps of 16 (8 columns of P, 2048 bytes of V); acc = 0: the first overwrites.
+// O += P V for kSteps * 16 keys (8 columns of P and 2048 bytes of V each); acc = 0: the first overwrites.
+template <int kSteps>
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred f, t, e;\n\t.reg .b32 r, a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "{\n\t.reg .pred f, t, e;\n\t.reg .b32 r, a1;\n\t.reg .b64 b1;\n\t"
       "elect.sync r|e, 0xffffffff;\n\t"
       "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
-      "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.s64 b1, %2, 128;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+  if constexpr (kSteps > 2) mma_values<kSteps - 2>(d, a + 16, b + 256, idesc, 1u);
 }
 __device__ __forceinline__ void commit_e(uint64_t* bar) {
   asm volatile(
@@ -205,15 +207,31 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ps = p.c.page_size, H = p.c.kv_heads, G = p.q_heads / H;
 
-  // the longest (last) row tiles first, so that the short ones fill the end of the launch
   grid_dependency_launch();
+  // heads, then chunks, then row tiles from the last (longest) to the first, then sequences from the
+  // longest to the shortest (up to kSorted of them): the work that starts last is short, and the launch
+  // ends evenly
   unsigned idx = blockIdx.x;
   const int h = int(idx % unsigned(H));
   idx /= unsigned(H);
-  const int b = int(idx % unsigned(p.b.num_seqs));
-  idx /= unsigned(p.b.num_seqs);
   const int split = int(idx % unsigned(p.tc_splits));
-  const int tile = row_tiles - 1 - int(idx / unsigned(p.tc_splits));
+  idx /= unsigned(p.tc_splits);
+  const int tile = row_tiles - 1 - int(idx % unsigned(row_tiles));
+  int b = int(idx / unsigned(row_tiles));
+  if (p.b.num_seqs > 1 && p.b.num_seqs <= kSorted) {
+    // the sequence of rank b: each of the first threads finds the rank of its own
+    int* lens = reinterpret_cast<int*>(smem);  // (Q comes here later)
+    if (tid < p.b.num_seqs) lens[tid] = __ldg(p.b.seq_lens + tid);
+    __syncthreads();
+    if (tid < p.b.num_seqs) {
+      const int mine = lens[tid];
+      int rank = 0;
+      for (int i = 0; i < p.b.num_seqs; ++i) rank += lens[i] > mine || (lens[i] == mine && i < tid);
+      if (rank == b) bars->sorted = tid;
+    }
+    __syncthreads();
+    b = bars->sorted;
+  }
 
   const int64_t row0 = int64_t(tile) * kTcRows;
   const Rows s = sequence_rows(p, b, row0, kTcRows, G);
@@ -387,7 +405,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       tc_fence_after();
       for (int w = 0; w < n_tiles; ++w) scores(w, 0);
     }
-    // P V of step j (each half of the keys as soon as its P is there), then the row tile's next
+    // P V of step j (each part of the keys as soon as its P is there), then the row tile's next
     // scores, which overwrite P
     for (int j = 0; ok && j < n_steps; ++j) {
       const int slot = (2 * j + 1) % G_::kTiles;
@@ -398,11 +416,11 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         ok = warp_wait(&bars->p_full[w][0], j & 1, abort, p.status, kStPFull);
         if (!ok) break;
         tc_fence_after();
-        mma_values(t_o, t_p, v, kIdO, j > 0 ? 1u : 0u);
+        mma_values<kPFirst / 16>(t_o, t_p, v, kIdO, j > 0 ? 1u : 0u);
         ok = warp_wait(&bars->p_full[w][1], j & 1, abort, p.status, kStPFull);
         if (!ok) break;
         tc_fence_after();
-        mma_values(t_o, t_p + 32, v + uint64_t((64 * 128) >> 4), kIdO, 1u);
+        mma_values<(kKeys - kPFirst) / 16>(t_o, t_p + kPFirst / 2, v + uint64_t((kPFirst * 128) >> 4), kIdO, 1u);
         if (w == n_tiles - 1) commit_e(&bars->t_empty[slot]);
         if (j + 1 < n_steps) {
           if (w == 0) ok = wait_tile(2 * j + 2, kStKFull);
@@ -606,11 +624,11 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             pk[e / 2 + 1] = h2(v.x, v.y);
           }
           tmem_st16(t_s + uint32_t(i / 2), pk);
-          if (i % 64 == 32) {
+          if (i + 32 == kPFirst || i + 32 == kKeys) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[w][i / 64]);
+            if (lane == 0) mbar_arrive(&bars->p_full[w][i + 32 == kKeys ? 1 : 0]);
           }
         }
         l2 = __fadd2_rn(l2, __fadd2_rn(sum0, sum1));
