@@ -280,15 +280,14 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   uint4 qv[kRowIter];
   int64_t my_row = 0;  // (token, head) index of this thread's row in q and out
   if (warp < 4 * n_tiles) {
-    const unsigned ti = (rem0 + unsigned(tid)) / Gu, hi = rem0 + unsigned(tid) - ti * Gu;
+    // (rows that are not there read the last one: loads under a condition were waited for one by one)
+    const unsigned r = rem0 + unsigned(min(tid, rows - 1)), ti = r / Gu, hi = r - ti * Gu;
     my_row = (tok0 + ti) * p.q_heads + h * G + int(hi);
-    const int64_t my_off = (tok0 + ti) * p.q_stride + int64_t(h * G + int(hi)) * D;
+    const uint16_t* mine = static_cast<const uint16_t*>(p.q) + (tok0 + ti) * p.q_stride + int64_t(h * G + int(hi)) * D;
 #pragma unroll
     for (int i = 0; i < kRowIter; ++i) {
-      const int64_t off = __shfl_sync(0xffffffffu, my_off, i * kRpi + sub);
-      qv[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (warp * 32 + i * kRpi + sub < rows)
-        qv[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off) + c8);
+      const uint64_t from = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), i * kRpi + sub);
+      qv[i] = __ldg(reinterpret_cast<const uint4*>(from) + c8);
     }
   }
 
@@ -533,7 +532,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
         for (int o = kLpr / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const int qe = row_exponent(amax);
-        const float f = sign * exp2i(-qe);
+        const float f = r < rows ? sign * exp2i(-qe) : 0.0f;
         const uint32_t dst = sbase + uint32_t((r >> 7) * G_::kQBytes + (c8 >> 3) * 16384 + (r & 127) * 128);
         sts128(dst + uint32_t(((c8 & 7) ^ (r & 7)) << 4), h2(x0.x * f, x0.y * f), h2(x1.x * f, x1.y * f),
                h2(x2.x * f, x2.y * f), h2(x3.x * f, x3.y * f));
