@@ -20,9 +20,13 @@
 // stay below 2^15, within fp16, and relative rounding is the same): O and the sum are rescaled that
 // rarely. Probabilities are rounded to fp16 (2^-11).
 //
-// Roles, 512 threads: warps 0-3 and 4-7 softmax of row tile 0 and 1 (its Q before, its output
-// after), 8-11 converters, 12 TMA producer, 13 MMA issuer (owns TMEM). TMEM: O 2 x D columns, S
-// 2 x 128 columns (P overwrites the first half of its S). Every wait is bounded.
+// Roles, 512 threads: warp 0 MMA issuer (owns TMEM), 1 TMA producer, 4-7 and 8-11 softmax of row
+// tile 0 and 1 (its Q before, its output after), 12-15 converters. The issuer comes first and waits as
+// seldom as it can: its barrier operations queue behind the exponentials of its scheduler's softmax
+// warps (about 200 clocks each), and a step of one row tile is a chain of softmax (2000 clocks), its
+// hand-over, P V and S (1024), and their hand-over back; the two row tiles' chains overlap, about 3800
+// clocks a step. TMEM: O 2 x D columns, S 2 x 128 columns (P overwrites the first half of its S).
+// Every wait is bounded.
 #include <cstdint>
 #include <type_traits>
 
@@ -36,9 +40,8 @@ using namespace kv;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kKeys = 128;  // keys of a step
-constexpr int kPFirst = 96; // keys whose probabilities are handed over first
 constexpr int kSorted = 256;  // sequences that are taken in order of length
-constexpr int kWarpConv0 = 8, kWarpProducer = 12, kWarpMma = 13;
+constexpr int kWarpMma = 0, kWarpProducer = 1, kWarpSoft0 = 4, kWarpConv0 = 12;
 // Register split (setmaxnreg): launched at 128 per thread; 2 softmax warpgroups, the converters, the rest
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsConv = 72, kRegsLow = 40;
 static_assert(128 * (2 * kRegsSoftmax + kRegsConv + kRegsLow) <= kThreads * kRegsLaunch, "register split");
@@ -70,7 +73,7 @@ struct Bars {
   // unit u = 2j is K of step j, u = 2j + 1 V of step j
   uint64_t raw_full[4], raw_empty[4];  // codes of unit u, slot u % 4
   uint64_t t_full[3], t_empty[3];      // converted tile of unit u, slot u % 3
-  uint64_t s_full[2], p_full[2][2];  // row tile; P in two parts
+  uint64_t s_full[2], p_full[2];     // row tile
   uint64_t o_full[2];                // row tile: O complete
   uint64_t q_full;
   uint64_t mma_done;
@@ -263,7 +266,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       mbar_init(&bars->t_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      for (int k = 0; k < 2; ++k) mbar_init(&bars->p_full[i][k], 4);
+      mbar_init(&bars->p_full[i], 4);
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->o_full[i], 1);
     }
@@ -279,9 +282,9 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const int c8 = lane % kLpr, sub = lane / kLpr;
   uint4 qv[kRowIter];
   int64_t my_row = 0;  // (token, head) index of this thread's row in q and out
-  if (warp < 4 * n_tiles) {
+  if (warp >= kWarpSoft0 && warp < kWarpSoft0 + 4 * n_tiles) {
     // (rows that are not there read the last one: loads under a condition were waited for one by one)
-    const unsigned r = rem0 + unsigned(min(tid, rows - 1)), ti = r / Gu, hi = r - ti * Gu;
+    const unsigned r = rem0 + unsigned(min(tid - kWarpSoft0 * 32, rows - 1)), ti = r / Gu, hi = r - ti * Gu;
     my_row = (tok0 + ti) * p.q_heads + h * G + int(hi);
     const uint16_t* mine = static_cast<const uint16_t*>(p.q) + (tok0 + ti) * p.q_stride + int64_t(h * G + int(hi)) * D;
 #pragma unroll
@@ -404,27 +407,20 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       tc_fence_after();
       for (int w = 0; w < n_tiles; ++w) scores(w, 0);
     }
-    // P V of step j (each part of the keys as soon as its P is there), then the row tile's next
-    // scores, which overwrite P
+    // P V of step j, then the row tile's next scores, which overwrite P
     for (int j = 0; ok && j < n_steps; ++j) {
       const int slot = (2 * j + 1) % G_::kTiles;
       const uint64_t v = desc_lbo(sbase + uint32_t(G_::kOffTile + slot * G_::kTile), kKeys * 128);
-      ok = wait_tile(2 * j + 1, kStVFull);
+      // K of the next step, whose conversion follows V's of this one (or V alone in the last step)
+      ok = wait_tile(j + 1 < n_steps ? 2 * j + 2 : 2 * j + 1, j + 1 < n_steps ? kStKFull : kStVFull);
       for (int w = 0; ok && w < n_tiles; ++w) {
         const uint32_t t_o = tmem + G_::kColO + uint32_t(w * D), t_p = tmem + G_::kColS + uint32_t(w * 128);
-        ok = warp_wait(&bars->p_full[w][0], j & 1, abort, p.status, kStPFull);
+        ok = warp_wait(&bars->p_full[w], j & 1, abort, p.status, kStPFull);
         if (!ok) break;
         tc_fence_after();
-        mma_values<kPFirst / 16>(t_o, t_p, v, kIdO, j > 0 ? 1u : 0u);
-        ok = warp_wait(&bars->p_full[w][1], j & 1, abort, p.status, kStPFull);
-        if (!ok) break;
-        tc_fence_after();
-        mma_values<(kKeys - kPFirst) / 16>(t_o, t_p + kPFirst / 2, v + uint64_t((kPFirst * 128) >> 4), kIdO, 1u);
+        mma_values<8>(t_o, t_p, v, kIdO, j > 0 ? 1u : 0u);
         if (w == n_tiles - 1) commit_e(&bars->t_empty[slot]);
         if (j + 1 < n_steps) {
-          if (w == 0) ok = wait_tile(2 * j + 2, kStKFull);
-          if (!ok) break;
-          tc_fence_after();
           scores(w, j + 1);
         } else {
           commit_e(&bars->o_full[w]);
@@ -510,10 +506,10 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         mbar_arrive(&bars->t_full[tile_slot]);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp >= kWarpSoft0 && warp < kWarpSoft0 + 8) {
     // ---------------- softmax and output of row tile w ----------------
     setmaxnreg_inc<kRegsSoftmax>();
-    const int w = warp >> 2;
+    const int w = (warp - kWarpSoft0) >> 2, tr = tid - kWarpSoft0 * 32;  // row of the CTA
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + G_::kColS + uint32_t(w * 128), t_o = t_lane + G_::kColO + uint32_t(w * D);
     float c = 1.0f;   // factor of a score: z log2 e = S * c
@@ -524,7 +520,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       const float sign = p.scale == 0.0f ? 0.0f : (p.scale < 0.0f ? -1.0f : 1.0f);
 #pragma unroll
       for (int i = 0; i < kRowIter; ++i) {
-        const int r = warp * 32 + i * kRpi + sub;
+        const int r = (warp - kWarpSoft0) * 32 + i * kRpi + sub;
         const float2 x0 = unpack16(qv[i].x, kF16), x1 = unpack16(qv[i].y, kF16), x2 = unpack16(qv[i].z, kF16),
                      x3 = unpack16(qv[i].w, kF16);
         float amax = max3(fmaxf(fabsf(x3.x), fabsf(x3.y)), max3(fabsf(x0.x), fabsf(x0.y), fabsf(x1.x)),
@@ -541,11 +537,11 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->q_full);
-      const unsigned ti = (rem0 + unsigned(tid)) / Gu;
-      if (p.scale != 0.0f) c = fabsf(p.scale) * kLog2e * exp2i(bars->q_exp[tid]);
+      const unsigned ti = (rem0 + unsigned(tr)) / Gu;
+      if (p.scale != 0.0f) c = fabsf(p.scale) * kLog2e * exp2i(bars->q_exp[tr]);
       int64_t v = s.len;
       if (p.causal) v = min(v, s.len - s.n + i0 + int64_t(ti) + 1);
-      vis = tid < rows ? v - c0 : 0;
+      vis = tr < rows ? v - c0 : 0;
     }
     if (p.scale != 0.0f) c = fmaxf(c * exp2i(k_top - 6), 1e-37f);  // positive: -inf * c is -inf
     float m = -INFINITY;  // the row's maximum that the exponents are taken against (of S)
@@ -623,19 +619,17 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             pk[e / 2 + 1] = h2(v.x, v.y);
           }
           tmem_st16(t_s + uint32_t(i / 2), pk);
-          if (i + 32 == kPFirst || i + 32 == kKeys) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[w][i + 32 == kKeys ? 1 : 0]);
-          }
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[w]);
         l2 = __fadd2_rn(l2, __fadd2_rn(sum0, sum1));
       }
       if (ok && n_steps > 0) ok = warp_wait(&bars->o_full[w], 0, abort, p.status, kStOFull);
       if (ok) {
         tc_fence_after();
-        const int r = tid;
+        const int r = tr;
         const bool live = r < rows;
         const int64_t row = my_row;
         const float L = l2.x + l2.y;
@@ -674,7 +668,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             const int rr = i * kRpi + lane / kPieces;
             const uint4 y = lds128(mine + uint32_t(rr * D * 2) + uint32_t((piece ^ (rr & 7)) << 4));
             const int64_t to = __shfl_sync(0xffffffffu, my_row, rr);
-            if (warp * 32 + rr < rows)
+            if ((warp - kWarpSoft0) * 32 + rr < rows)
               *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to * D) + piece) = y;
           }
         } else {
