@@ -33,6 +33,16 @@ def _fits(t, dtype, device):
     return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
 
 
+def _empty(shape, dtype, device, stream):
+    """An output or a workspace that a call on `stream` (None: the current one) writes. It is
+    taken from that stream's memory: memory that another stream freed may still be read by what
+    is queued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
@@ -141,6 +151,11 @@ class FlatQuant:
         return int(v.value)
 
     def _inputs(self, x, P1, P2, allow_no_p2=False):
+        dev = torch.cuda.current_device() if isinstance(x, torch.Tensor) and x.is_cuda else -1
+        if (dev >= 0 and _fits(x, self.dtype, dev) and _fits(P1, self.dtype, dev) and _fits(P2, self.dtype, dev)
+                and x.shape == (self.K, self.M, self.N) and P1.shape == (self.M, self.M)
+                and P2.shape == (self.N, self.N)):
+            return P2
         _check_input("x", x, self.dtype)
         _check_input("P1", P1, self.dtype)
         if tuple(x.shape) != (self.K, self.M, self.N):
@@ -168,21 +183,21 @@ class FlatQuant:
         K, M, N = self.K, self.M, self.N
         if out is None:
             if out_dtype == "int8":
-                out = torch.empty((K, M * N), dtype=torch.int8, device=x.device)
+                out = _empty((K, M * N), torch.int8, x.device, stream)
             elif out_dtype == "int32":
-                out = torch.empty((K, M, N // 8), dtype=torch.int32, device=x.device)
+                out = _empty((K, M, N // 8), torch.int32, x.device, stream)
             else:
-                out = torch.empty((K, M * N // 2), dtype=torch.uint8, device=x.device)
+                out = _empty((K, M * N // 2), torch.uint8, x.device, stream)
         else:
             _check_output("out", out, K * M * N // (1 if out_dtype == "int8" else 2), x.device)
         if quant_scale is None:
-            quant_scale = torch.empty((K,), dtype=torch.float32, device=x.device)
+            quant_scale = _empty((K,), torch.float32, x.device, stream)
         else:
             _check_output("quant_scale", quant_scale, 4 * K, x.device, torch.float32)
         fmt = {"int32": _lib.FQ_OUT_INT32, "int8": _lib.FQ_OUT_INT8}.get(out_dtype, _lib.FQ_OUT_INT4)
         _lib.check(self._lib.fq_quantize_per_token(
-            self._h, _ptr(x), _ptr(P1), _ptr(P2), float(clip_ratio), fmt, _ptr(out),
-            _ptr(quant_scale), _stream_ptr(stream)), "fq_quantize_per_token")
+            self._h, x.data_ptr(), P1.data_ptr(), P2.data_ptr(), float(clip_ratio), fmt, out.data_ptr(),
+            quant_scale.data_ptr(), _raw_stream(stream, x.get_device())), "fq_quantize_per_token")
         return out, quant_scale
 
     def quantize_mx(self, x, P1, P2, dst_type_max=0.0, out=None, scales=None, stream=None):
@@ -286,7 +301,7 @@ def int8_matmul(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stat
     if a_scale.numel() != T or w_scale.numel() != O:
         raise ValueError("a_scale and w_scale must have one scale per row of a and of w")
     if out is None:
-        out = torch.empty((T, O), dtype=out_dtype, device=a.device)
+        out = _empty((T, O), out_dtype, a.device, stream)
     else:
         _check_output("out", out, T * O * out_dtype.itemsize, a.device, out_dtype)
     if status is not None:
@@ -425,7 +440,7 @@ class KVCache:
             qs = self._tokens("q", q, T, None, k.dtype)
             hq = q.shape[1]
             if q_out is None:
-                q_out = torch.empty((T, hq, self.head_dim), dtype=q.dtype, device=q.device)
+                q_out = _empty((T, hq, self.head_dim), q.dtype, q.device, stream)
             else:
                 _check_output("q_out", q_out, T * hq * self.head_dim * 2, q.device, q.dtype)
             q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
@@ -454,13 +469,13 @@ class KVCache:
         if max_seq_len is None:
             max_seq_len = batch.table_width * self.page_size
         if out is None:
-            out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+            out = _empty((T, hq, D), q.dtype, q.device, stream)
         else:
             _check_output("out", out, T * hq * D * 2, q.device, q.dtype)
         if lse is not None:
             _check_output("lse", lse, T * hq * 4, q.device, torch.float32)
         elif return_lse:
-            lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+            lse = _empty((T, hq), torch.float32, q.device, stream)
         sizes = (T, hq, batch.num_seqs, batch.table_width, max_q_len, max_seq_len)
         need = self._workspace_bytes.get(sizes)
         if need is None:
@@ -471,11 +486,7 @@ class KVCache:
             if len(self._workspace_bytes) >= 4096:
                 self._workspace_bytes.clear()
             need = self._workspace_bytes[sizes] = n.value
-        ws = None
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                ws.record_stream(stream)  # freed on this stream's clock, used on the other's
+        ws = _empty(need, torch.uint8, q.device, stream) if need else None
         st = self._lib.fq_kv_attention(
             ctypes.byref(self._desc), ctypes.byref(batch), T, _DT[q.dtype], q.data_ptr(), qs, hq, int(max_q_len),
             int(max_seq_len), float(scale if scale is not None else D ** -0.5), 1 if causal else 0, out.data_ptr(),

@@ -43,7 +43,8 @@ struct KvAttnParams {
   int tile_rows;     // rows of a CTA (8 or 16)
   int64_t tc_rows;   // sequences with more rows (new tokens * group) take the tensor-core kernel
   int tc_chunk, tc_splits;
-  int ws_splits;     // slots per row of the workspace: max(splits, tc_splits)
+  int cluster;       // the chunks of up to tile_rows rows are a cluster, which joins them itself
+  int ws_splits;     // slots per row of the workspace: most chunks that the join kernel joins
 };
 
 // How fq_kv_attention divides its work; the workspace follows from it.
@@ -51,6 +52,7 @@ struct KvAttnPlan {
   int chunk, splits, tile_rows, row_tiles;  // mma.sync kernel: tile_rows rows and one chunk per CTA; 0 tiles: not launched
   int tc_chunk, tc_splits, tc_row_tiles;    // tensor-core kernel: 256 rows and one chunk per CTA; 0: not launched
   int64_t tc_rows;
+  int cluster, ws_splits;                   // see KvAttnParams
   int64_t ws_bytes;
 };
 KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, int q_heads, int max_q_len,

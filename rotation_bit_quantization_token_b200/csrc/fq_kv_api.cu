@@ -131,7 +131,7 @@ fq_status fq_kv_attention(const fq_kv_cache* cache, const fq_kv_batch* batch, in
   p.max_q_len = max_q_len; p.causal = causal; p.fp16 = dtype == FQ_FP16; p.scale = float(scale);
   p.chunk = plan.chunk; p.splits = plan.splits; p.tile_rows = plan.tile_rows; p.tc_rows = plan.tc_rows;
   p.tc_chunk = plan.tc_chunk; p.tc_splits = plan.tc_splits;
-  p.ws_splits = plan.splits > plan.tc_splits ? plan.splits : plan.tc_splits;
+  p.cluster = plan.cluster; p.ws_splits = plan.ws_splits;
   const cudaError_t e = fq::launch_kv_attn(p, plan, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FQ_OK : fail(e);
 }

@@ -8,8 +8,9 @@
 // One CTA takes its rows and one chunk of keys; its four warps take tiles of 4096 / D keys in turn,
 // each through a ring of its own (TMA boxes of 128-byte rows, swizzled; no barrier between the
 // warps), with a running maximum, sum and output of its own; they are joined through shared memory
-// at the end. A sequence longer than one chunk is joined by a second kernel from partial results in
-// the workspace.
+// at the end. The chunks of a longer sequence are joined by their cluster, each CTA reading a share of
+// the others' results in shared memory, or, where they are too many, by a second kernel from partial
+// results in the workspace.
 //
 // Products are mma.sync with the keys (then the output columns) on the M side and the rows on N: with
 // 8 rows nothing is padded, and a thread holds a quarter of the output registers of the other
@@ -39,6 +40,7 @@ using namespace kv;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kMaxChunkBytes = 4096 * 128;  // of K in one chunk (V as much again)
+constexpr int kMaxCluster = 8;              // chunks that are joined in a cluster, at most
 
 enum : uint32_t { kStFull = 1u << 0 };
 
@@ -52,7 +54,8 @@ struct Geo {
   static constexpr int kMinBlocks = NT == 1 ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kOStride = D + 4;                    // floats per row of a warp's output
-  static_assert(kWarps * kRows * kOStride * 4 <= kRing, "outputs fit the ring");
+  static constexpr int kJoinAt = kWarps * kRows * kOStride * 4;  // the CTA's own result, for its cluster
+  static_assert(kJoinAt + kRows * kOStride * 4 <= kRing, "outputs fit the ring");
 };
 
 struct Shared {
@@ -83,6 +86,19 @@ template <int D>
 __device__ __forceinline__ uint32_t swz(int key, int d) {
   const uint32_t o = uint32_t(key * D + d);
   return o ^ (((o >> 7) & 7u) << 4);
+}
+
+// Words of the shared memory of a CTA of the cluster.
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
 }
 
 // Two E4M3 codes (the low and the high half of w) as two fp16 numbers each.
@@ -117,12 +133,20 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 
   grid_dependency_launch();
   unsigned idx = blockIdx.x;
+  int split = 0;
+  if (p.cluster) {  // the chunks of a row lie side by side
+    split = int(idx % unsigned(p.splits));
+    idx /= unsigned(p.splits);
+  }
   const int tile = int(idx % unsigned(row_tiles));
   idx /= unsigned(row_tiles);
   const int h = int(idx % unsigned(H));
   idx /= unsigned(H);
-  const int split = int(idx % unsigned(p.splits));
-  const int b = int(idx / unsigned(p.splits));
+  if (!p.cluster) {
+    split = int(idx % unsigned(p.splits));
+    idx /= unsigned(p.splits);
+  }
+  const int b = int(idx);
 
   const Rows s = sequence_rows(p, b, int64_t(tile) * kRowsTile, kRowsTile, G);
   if (tid == 0 && split == 0 && h == 0 && tile == 0 && p.status != nullptr && (!s.ok || s.n > p.max_q_len))
@@ -455,11 +479,13 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       }
   }
   __syncthreads();
-  if (*reinterpret_cast<volatile int*>(&sh->abort)) return;
+  const bool meet = p.cluster && !whole;
+  const bool gave_up = *reinterpret_cast<volatile int*>(&sh->abort) != 0;
+  if (gave_up && !meet) return;
   constexpr int kTpr = kThreads / kRowsTile;  // threads per row
   constexpr int kPer = D / kTpr;              // columns of a thread
   const int r = tid / kTpr, d0 = (tid % kTpr) * kPer;
-  if (r >= rows) return;
+  if (r >= rows && !meet) return;
   float M = -INFINITY;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh->m[w][r]);
@@ -474,6 +500,56 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     const float* x = reinterpret_cast<const float*>(smem) + (w * kRowsTile + r) * G_::kOStride + d0;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] += x[e] * f;
+  }
+  if (meet) {
+    // A CTA that gave up takes part as well (the others read its memory; the result is undefined),
+    // one without keys has left and is not read.
+    float* own = reinterpret_cast<float*>(smem + G_::kJoinAt) + r * G_::kOStride;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 4)
+      *reinterpret_cast<float4*>(own + d0 + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+    if (d0 == 0) *reinterpret_cast<float2*>(own + D) = make_float2(M, L);
+    __syncwarp();
+    cluster_sync();
+    const int n = int((s.end + p.chunk - 1) / p.chunk);
+    for (int i = split * kThreads + tid; i < rows * (D / 4); i += n * kThreads) {
+      const int rr = i / (D / 4), col = i % (D / 4);
+      const uint32_t at = smem_u32(smem) + uint32_t(G_::kJoinAt + rr * G_::kOStride * 4);
+      float2 ml[kMaxCluster];
+      float4 v[kMaxCluster];
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        ml[c] = make_float2(-INFINITY, 0.0f);
+        v[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c < n) {
+          const uint32_t from = remote_addr(at, uint32_t(c));
+          ml[c] = ld_cluster2(from + D * 4);
+          v[c] = ld_cluster4(from + col * 16);
+        }
+      }
+      float Mc = -INFINITY, Lc = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) Mc = fmaxf(Mc, ml[c].x);
+      const float mu = Mc == -INFINITY ? 0.0f : Mc;
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        const float f = fast_exp2(ml[c].x - mu);
+        Lc += ml[c].y * f;
+        sum.x += v[c].x * f;
+        sum.y += v[c].y * f;
+        sum.z += v[c].z * f;
+        sum.w += v[c].w * f;
+      }
+      const float inv = Lc > 0.0f ? 1.0f / Lc : 0.0f;
+      const int64_t row = (s.t_first + (row0 + rr) / G) * p.q_heads + h * G + (row0 + rr) % G;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + 4 * col) =
+          make_uint2(pack16(sum.x * inv, sum.y * inv, p.fp16), pack16(sum.z * inv, sum.w * inv, p.fp16));
+      if (p.lse != nullptr && col == 0) p.lse[row] = Lc > 0.0f ? (mu + log2f(Lc)) * kLn2 : -INFINITY;
+    }
+    __syncwarp();
+    cluster_sync();  // none leaves while its memory is read
+    return;
   }
   const int64_t row = (s.t_first + (row0 + r) / G) * p.q_heads + h * G + (row0 + r) % G;
   if (whole) {
@@ -496,7 +572,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   }
 }
 
-// Joins the chunks of the rows that had more than one. D / 4 threads lie side by side on a row's
+// Joins the chunks of the rows that had more than one and no cluster. D / 4 threads lie side by side on a row's
 // columns; kWide: a CTA takes one row, its groups of D / 4 threads different chunks of it (few rows
 // with hundreds of chunks: a group alone took longer than the attention itself); else every group
 // has a row of its own (many rows with a few chunks).
@@ -537,7 +613,7 @@ kv_attn_join_kernel(const KvAttnParams p, const int few) {
   const bool tc = takes_tc(p, n_new, G);
   const int tile_rows = tc ? kTcRows : p.tile_rows, chunk = tc ? p.tc_chunk : p.chunk;
   const Rows s = sequence_rows(p, lo, (i * G + hq % G) / tile_rows * tile_rows, tile_rows, G);
-  live = live && i >= 0 && i < s.n && i < p.max_q_len && s.end > chunk;
+  live = live && i >= 0 && i < s.n && i < p.max_q_len && s.end > chunk && (tc || !p.cluster);
   // every thread waits, also where there is nothing to do: this kernel must not end before the
   // attention does, or what comes after it could start beside that
   grid_dependency_wait();
@@ -610,8 +686,23 @@ cudaError_t launch_rows(const KvAttnParams& p, const KvAttnPlan& plan, cudaStrea
   if (e != cudaSuccess) return e;
   const int64_t grid = int64_t(plan.row_tiles) * p.c.kv_heads * plan.splits * p.b.num_seqs;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  kv_attn_kernel<D, NT><<<unsigned(grid), kThreads, smem, stream>>>(map_k, map_v, p, plan.row_tiles);
-  return cudaGetLastError();
+  if (!p.cluster) {
+    kv_attn_kernel<D, NT><<<unsigned(grid), kThreads, smem, stream>>>(map_k, map_v, p, plan.row_tiles);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(plan.splits);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NT>, map_k, map_v, p, plan.row_tiles);
 }
 
 template <int D>
@@ -643,13 +734,10 @@ cudaError_t launch_attn(const KvAttnParams& p, const KvAttnPlan& plan, cudaStrea
   return cudaSuccess;
 }
 
-// Chunk of keys for `ctas` CTAs of one chunk each over max_len keys: chunks until there are
-// `want` CTAs, of at least `least` keys.
-int64_t chunk_for(int64_t max_len, int64_t ctas, int64_t want, int64_t least, int64_t most) {
-  const int64_t n = (want + ctas - 1) / ctas;
-  int64_t chunk = (max_len + n - 1) / n;
-  chunk = (chunk + 127) / 128 * 128;
-  return chunk < least ? least : (chunk > most ? most : chunk);
+// Keys of a chunk where max_len keys are to be `n` chunks.
+int chunk_for(int64_t max_len, int64_t n, int64_t least) {
+  const int64_t chunk = ((max_len + n - 1) / n + 127) / 128 * 128, most = 1 << 24;
+  return int(chunk < least ? least : (chunk > most ? most : chunk));
 }
 
 }  // namespace
@@ -659,6 +747,10 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
   KvAttnPlan plan{};
   const int G = q_heads / c.kv_heads;
   const int64_t rows = int64_t(max_q_len) * G;  // of one sequence, at most
+  // Above 64 rows the tensor-core kernel: both take about as long there (64 sequences of 512 keys,
+  // 64 rows: 81 us here, 75 there; 8 of 4096: 63 and 64; 8 of 16384: 190 and 216); with 128 rows
+  // this one takes twice as long (156, 104, 360 us for 78, 67, 200), with 32 that one (43, 39, 109
+  // for 75, 62, 206).
   plan.tc_rows = 64;
   const int64_t few = b.num_seqs == 1 && rows > plan.tc_rows ? 0 : (rows < plan.tc_rows ? rows : plan.tc_rows);
   if (few == 0) plan.tc_rows = 0;  // one sequence: whatever its length, one kernel
@@ -668,21 +760,31 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
   plan.chunk = plan.tc_chunk = 0x7FFFFF80;
   if (plan.row_tiles > 0) {
     const int64_t ctas = int64_t(b.num_seqs) * c.kv_heads * plan.row_tiles;
-    // the machine filled once (three CTAs on an SM), or chunks of 1 MB, whichever is smaller: a
-    // ragged batch then ends evenly (64 sequences of 500-16000: 197 us with chunks of 2 MB, 182 with
-    // 1 MB), and a CTA's start and end (about 3 us) and the join stay small beside its chunk
-    plan.chunk = int(chunk_for(max_seq_len, ctas, 3 * int64_t(num_sms), 256, kMaxChunkBytes / c.head_dim));
+    // One wave of CTAs (three or two on an SM) where that takes chunks of at most 1 MB (keys and
+    // values): not a CTA more, since a second wave of a few costs a whole one (16 sequences of 8000
+    // tokens, 8 heads: 48 us with 384 CTAs, 62 with 512). Else chunks of 0.5 MB (16 rows: 1 MB), so
+    // that a ragged batch ends evenly: 64 sequences of 500-16000 tokens 197 us with chunks of 2 MB,
+    // 174 with 1, 169 with 0.5, 172 with 0.25, where starts and ends of CTAs (3 us) begin to show.
+    const int64_t wave = int64_t(plan.tile_rows == 8 ? 3 : 2) * num_sms, n = wave / ctas;
+    const int64_t most = kMaxChunkBytes / c.head_dim;
+    plan.chunk = chunk_for(max_seq_len, n > 1 ? n : 1, 256);
+    if (n < 1 || plan.chunk > most) plan.chunk = int(plan.tile_rows == 8 ? most / 2 : most);
     plan.splits = int((max_seq_len + plan.chunk - 1) / plan.chunk);
+    // Joined in a cluster: no workspace and no second kernel (4 us of host time), a sequence
+    // of 700 tokens 7.7 us for 8.4, of 1500 7.8 for 9.7. In one wave only, since a cluster
+    // waits for room for all its CTAs: 16 sequences of 16000 in 512 CTAs 116 us for 107.
+    plan.cluster = plan.splits > 1 && plan.splits <= kMaxCluster && ctas * plan.splits <= wave;
   }
   if (rows > plan.tc_rows) {
     plan.tc_row_tiles = int((rows + kTcRows - 1) / kTcRows);
     // the token rows bound the CTAs that have work, whatever the longest sequence
     const int64_t tiles = (T * G + kTcRows - 1) / kTcRows;
-    plan.tc_chunk = int(chunk_for(max_seq_len, tiles * c.kv_heads, 2 * int64_t(num_sms), 1024, 1 << 24));
+    const int64_t ctas = tiles * c.kv_heads;
+    plan.tc_chunk = chunk_for(max_seq_len, (2 * int64_t(num_sms) + ctas - 1) / ctas, 1024);
     plan.tc_splits = int((max_seq_len + plan.tc_chunk - 1) / plan.tc_chunk);
   }
-  const int64_t slots = plan.splits > plan.tc_splits ? plan.splits : plan.tc_splits;
-  plan.ws_bytes = slots > 1 ? T * q_heads * slots * int64_t(c.head_dim + 4) * 4 : 0;
+  plan.ws_splits = !plan.cluster && plan.splits > plan.tc_splits ? plan.splits : plan.tc_splits;
+  plan.ws_bytes = plan.ws_splits > 1 ? T * q_heads * plan.ws_splits * int64_t(c.head_dim + 4) * 4 : 0;
   return plan;
 }
 

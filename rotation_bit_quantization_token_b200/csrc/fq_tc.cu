@@ -863,8 +863,8 @@ tc_kernel(const __grid_constant__ CUtensorMap tmap, const TcParams p) {
           for (int c = 0; c < nbk; ++c) {
             const int sg = c0 + c;
             const float2 F2 = make_float2(Fseg[sg], Fseg[sg]);
-            uint32_t words[2] = {0u, 0u};
-            uint32_t words8[4];  // INT8 codes
+            [[maybe_unused]] uint32_t words[2] = {0u, 0u};
+            [[maybe_unused]] uint32_t words8[4];  // INT8 codes
 #pragma unroll
             for (int wd = 0; wd < 2; ++wd) {
               const float* w = d + c * 16 + wd * 8;

@@ -588,3 +588,66 @@ def test_attention_loose_bounds():
     a = one.cache().attention(q, *one.batch(), max_q_len=3)
     b = one.cache().attention(q, *one.batch(), max_q_len=200)
     assert (a[:3].float() - b[:3].float()).abs().max() <= 2.0 ** -9 * a[:3].float().abs().max()
+
+
+def test_memory_of_the_given_stream():
+    """Outputs and workspaces of a call on another stream are not memory that the current stream
+    has freed but still has to read."""
+    s = Setup([1], [5000], H=1, D=64, page=64, seed=60).fill()
+    cache, (cu, lens, table) = s.cache(), s.batch()
+    q = torch.randn(1, 2, 64, device="cuda").to(torch.bfloat16)
+    k = torch.randn(1, 1, 64, device="cuda").to(torch.bfloat16)
+    a = torch.ones(3, 64, dtype=torch.int8, device="cuda")
+    sc = torch.ones(3, device="cuda")
+    fq, x = FlatQuant(3, 16, 16), torch.randn(3, 16, 16, device="cuda").to(torch.bfloat16)
+    eye = torch.eye(16, device="cuda").to(torch.bfloat16)
+    st = torch.cuda.Stream()
+    calls = [lambda: cache.attention(q, cu, lens, table, 1, return_lse=True, stream=st),
+             lambda: cache.append(k, k, cu, lens, table, q=q, stream=st),
+             lambda: int8_matmul(a, sc, a, sc, stream=st),
+             lambda: fq.quantize_per_token(x, eye, eye, out_dtype="int8", stream=st)]
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        held = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in (8, 256, 1024, 4096, 16384, 65536)
+                for _ in range(64)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(40_000_000)  # about 20 ms
+        copies = [h.clone() for h in held]
+        del held  # free, and read by the copies that are still queued
+        call()
+        torch.cuda.synchronize()
+        assert all(bool((c == 7).all()) for c in copies)
+
+
+@pytest.mark.parametrize("G,D,causal", [(1, 128, True), (4, 64, True), (8, 128, False), (16, 64, True)])
+def test_attention_few_chunks(G, D, causal):
+    """Two to eight chunks of a sequence, beside sequences of one chunk and of none."""
+    s = Setup([1, 1, 0, 2, 1, 1], [299, 1023, 0, 1500, 256, 0], H=2, D=D, page=64, seed=61).fill()
+    _check_attention(s, torch.bfloat16, G, causal=causal, tail=2)
+    _check_attention(s, torch.float16, G, causal=causal, max_seq_len=s.width * 64)
+
+
+def test_attention_few_chunks_of_many_sequences():
+    """More sequences and heads than one wave of CTAs, the longest of a few chunks."""
+    ctx = [3, 0, 70] * 19 + [4200, 2047, 2048]
+    s = Setup([1] * 60, ctx, H=8, D=128, page=128, seed=62).fill()
+    _check_attention(s, torch.bfloat16, 1)
+
+
+def test_attention_chunk_with_a_page_outside():
+    """A page outside the cache in one of a sequence's chunks: its keys are left out, the others join."""
+    s = Setup([1], [899], H=1, D=64, page=16, seed=63).fill()
+    cache = s.cache()
+    q = torch.randn(1, 2, 64, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    cu, lens, table = s.batch()
+    t = table.clone()
+    t[0, 20:36] = -7  # the second chunk's pages, all of them
+    out, lse = cache.attention(q, cu, lens, t, max_q_len=1, scale=0.125, return_lse=True)
+    assert cache.device_status() == _lib.FQ_KV_BAD_BATCH
+    k, v = osv.kv_values(s.k, s.ks, s.table[0], 900)[:, 0], osv.kv_values(s.v, s.vs, s.table[0], 900)[:, 0]
+    keep = [j for j in range(900) if not 20 <= j // 16 < 36]
+    z = 0.125 * f64(q[0]) @ k[keep].T
+    assert np.allclose(f64(lse[0]), np.log(np.exp(z).sum(-1)), atol=1e-5)
+    p = np.exp(z) / np.exp(z).sum(-1, keepdims=True)
+    assert np.allclose(f64(out[0]), p @ v[keep], rtol=2.0 ** -7, atol=2e-3)
