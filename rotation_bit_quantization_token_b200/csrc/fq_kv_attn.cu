@@ -747,10 +747,9 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
   KvAttnPlan plan{};
   const int G = q_heads / c.kv_heads;
   const int64_t rows = int64_t(max_q_len) * G;  // of one sequence, at most
-  // Above 64 rows the tensor-core kernel: both take about as long there (64 sequences of 512 keys,
-  // 64 rows: 81 us here, 75 there; 8 of 4096: 63 and 64; 8 of 16384: 190 and 216); with 128 rows
-  // this one takes twice as long (156, 104, 360 us for 78, 67, 200), with 32 that one (43, 39, 109
-  // for 75, 62, 206).
+  // Above 64 rows the tensor-core kernel; there the two are about even (64 sequences of 512 keys, 64
+  // rows: 81 us here and 75 there; 8 of 16384: 190 and 180). With 128 rows this one takes twice as
+  // long (156 us for 78; 360 for 159), with 32 that one does (43 for 75; 109 for 206).
   plan.tc_rows = 64;
   const int64_t few = b.num_seqs == 1 && rows > plan.tc_rows ? 0 : (rows < plan.tc_rows ? rows : plan.tc_rows);
   if (few == 0) plan.tc_rows = 0;  // one sequence: whatever its length, one kernel
@@ -777,10 +776,12 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
   }
   if (rows > plan.tc_rows) {
     plan.tc_row_tiles = int((rows + kTcRows - 1) / kTcRows);
-    // the token rows bound the CTAs that have work, whatever the longest sequence
-    const int64_t tiles = (T * G + kTcRows - 1) / kTcRows;
-    const int64_t ctas = tiles * c.kv_heads;
-    plan.tc_chunk = chunk_for(max_seq_len, (2 * int64_t(num_sms) + ctas - 1) / ctas, 1024);
+    // about one wave of CTAs, not two (512 new tokens of 8192 83 us, 118 with twice as many chunks; 4
+    // times 256 of 4096 77 and 130), of 1024 keys or more (1000 new of 4000, two heads: 35 us, 54 with
+    // 2048; 16 times 64 of 2000 the same). The token rows bound the CTAs that have work, whatever the
+    // longest sequence.
+    const int64_t ctas = (T * G + kTcRows - 1) / kTcRows * c.kv_heads, n = num_sms / ctas;
+    plan.tc_chunk = chunk_for(max_seq_len, n > 1 ? n : 1, 1024);
     plan.tc_splits = int((max_seq_len + plan.tc_chunk - 1) / plan.tc_chunk);
   }
   plan.ws_splits = !plan.cluster && plan.splits > plan.tc_splits ? plan.splits : plan.tc_splits;

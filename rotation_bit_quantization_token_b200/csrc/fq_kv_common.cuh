@@ -71,6 +71,10 @@ struct Rows {
   int64_t end;      // keys seen by at least one of the rows
   bool ok;
 };
+// a / b for a >= 0 (a 64-bit division takes several times as long as a 32-bit one).
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return (a >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
 __device__ __forceinline__ Rows sequence_rows(const KvAttnParams& p, int b, int64_t row0, int count, int G) {
   Rows r;
   r.t_first = __ldg(p.b.cu_new + b);
@@ -79,7 +83,7 @@ __device__ __forceinline__ Rows sequence_rows(const KvAttnParams& p, int b, int6
   r.ok = r.n >= 0 && r.t_first >= 0 && r.t_first + r.n <= p.T;
   r.ok = r.ok && r.len >= 0 && r.len <= p.max_seq_len && r.n <= r.len;
   if (!r.ok) r.n = 0;
-  const int64_t last = min((row0 + count - 1) / G, r.n - 1);
+  const int64_t last = min(quotient(row0 + count - 1, G), r.n - 1);
   r.end = p.causal ? min(r.len, r.len - r.n + last + 1) : r.len;
   if (r.end < 0) r.end = 0;
   return r;
