@@ -236,7 +236,8 @@ typedef struct {
  * A page that already holds tokens of the sequence keeps the larger of its exponent and the new
  * tokens'; when it grows, the codes of the older tokens are rounded once more (exact but for
  * codes that become subnormal). Rows that belong to no token are not written. The pages that
- * receive tokens belong to one sequence each: two sequences appending to one page race.
+ * receive tokens are distinct, in one sequence and between sequences: two appends to one page
+ * race (attention may share pages).
  *   status      a device word, or NULL
  * Strides are multiples of 8 elements, pointers 16-byte aligned. Allocates nothing;
  * asynchronous on stream; deterministic. Errors: FQ_ERR_NULLPTR, FQ_ERR_INVALID, FQ_ERR_CUDA. */
@@ -267,8 +268,12 @@ FQ_API fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch
  *               0). It holds partial results during the call only; calls that may overlap (on
  *               two streams, or two captured graphs) need one each
  * Sums, maxima and the softmax are float32. Keys and values enter the products exactly (an E4M3
- * code is an fp16 number); queries too, scaled by a power of two per row; the probabilities are
- * rounded to fp16 for the second product. Stale rows of a page (behind the last token) are never
+ * code is an fp16 number), queries too, scaled by a power of two per row, but for elements 2^-29
+ * below the row's largest; the probabilities are rounded to fp16 for the second product. Sequences
+ * of more than 64 (token, query head) pairs per key / value head are computed in units of the
+ * largest page scale among up to some thousands of their tokens: codes of pages 2^-21 of it or
+ * less lose low bits there. Scores past the float32 range and NaN in q are outside the contract.
+ * Stale rows of a page (behind the last token) are never
  * used, whatever they hold. Allocates nothing; asynchronous on stream; deterministic. Errors:
  * FQ_ERR_NULLPTR, FQ_ERR_INVALID (also a workspace that is too small), FQ_ERR_CUDA. */
 FQ_API fq_status fq_kv_attention(const fq_kv_cache *cache, const fq_kv_batch *batch, int64_t T, fq_dtype dtype,

@@ -785,7 +785,9 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
     plan.tc_splits = int((max_seq_len + plan.tc_chunk - 1) / plan.tc_chunk);
   }
   plan.ws_splits = !plan.cluster && plan.splits > plan.tc_splits ? plan.splits : plan.tc_splits;
-  plan.ws_bytes = plan.ws_splits > 1 ? T * q_heads * plan.ws_splits * int64_t(c.head_dim + 4) * 4 : 0;
+  // (sizes that no memory holds: more than any workspace has, not a number that wrapped)
+  const int64_t rows_bytes = T * q_heads * int64_t(c.head_dim + 4) * 4;
+  plan.ws_bytes = plan.ws_splits <= 1 ? 0 : (rows_bytes > INT64_MAX / plan.ws_splits ? INT64_MAX : rows_bytes * plan.ws_splits);
   return plan;
 }
 
