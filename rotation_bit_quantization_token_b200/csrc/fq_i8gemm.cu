@@ -652,19 +652,27 @@ template <int kBT, typename Out>
 cudaError_t launch_tile(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
   using G = Geo<kBT, true>;
   const int64_t tiles = ((g.O + kBO - 1) / kBO) * ((g.T + kBT - 1) / kBT), nk = (g.L + kBK - 1) / kBK;
-  // split K until every SM has its CTAs, as long as each CTA keeps four stages of work
+  // Split K while that takes no SM a second CTA (1 x 14336 x 4096, 112 tiles: whole 14.5 us, in two
+  // 15.4; 1 x 4096 x 4096, 32 tiles: whole 13.2, in four 8.5, in eight 10.3) and as long as each CTA keeps
+  // four stages of work (4 x 2048 x 2048: 5.8 us with four, 6.6 with eight), or eight where the partial
+  // sums are 128 KB (300 x 1024 x 1024: whole 9.9 us, in two 11.2).
+  constexpr int kLeast = kBT == 256 ? 8 : 4;
   int split = 1;
-  while (split < G::kMaxSplit && tiles * split * 2 <= num_sms * G::kMinBlocks && nk >= split * 2 * 4) split *= 2;
+  while (split < G::kMaxSplit && tiles * split * 2 <= num_sms && nk >= split * 2 * kLeast) split *= 2;
   return split > 1 ? launch_t<kBT, Out, true>(g, split, num_sms, stream) : launch_t<kBT, Out, false>(g, 1, num_sms, stream);
 }
 
 template <typename Out>
 cudaError_t launch_out(const I8GemmParams& g, int num_sms, cudaStream_t stream) {
+  // the narrowest tile that takes all tokens: 1 x 14336 x 4096 15 us with 16 columns, 20 with 64;
+  // 16 x 6144 x 4096 10 and 13; 100 x 6144 x 4096 14 us with 128, 18 with 256
   if (g.T <= 16) return launch_tile<16, Out>(g, num_sms, stream);
   if (g.T <= 32) return launch_tile<32, Out>(g, num_sms, stream);
   if (g.T <= 64) return launch_tile<64, Out>(g, num_sms, stream);
   if (g.T <= 128) return launch_tile<128, Out>(g, num_sms, stream);
-  // pairs where their tiles come close to filling the machine
+  // Pairs where their tiles come close to filling the machine: 1024 x 6144 x 4096 (96 tiles) 28.5 us, 32.4
+  // with tiles of one CTA; 1024 x 4096 x 4096 (64) 19.3 and 20.5; 768 x 4096 x 4096 (48 tiles) 19.0 and
+  // 20.0, but 333 x 4099 x 8192 (34) 26.5 and 25.4, split.
   const int64_t pairs = ((g.O + kPairO - 1) / kPairO) * ((g.T + kPairT - 1) / kPairT);
   if (pairs * 10 >= int64_t(num_sms / 2) * 7) return launch_pair<Out>(g, num_sms, stream);
   return launch_tile<256, Out>(g, num_sms, stream);

@@ -236,3 +236,11 @@ def test_rotated_linear_layer(K, M, N, O):
     full = oracle.rotate(f(x), f(P1), f(P2)).reshape(K, -1) @ (w.astype(np.float64) * sw[:, None].astype(np.float64)).T
     bound = 0.51 * s[:, None] * np.abs(w.astype(np.float64)).sum(1)[None, :] * sw[None, :]
     assert np.all(np.abs(C.double().cpu().numpy() - full) <= bound)
+
+
+@pytest.mark.parametrize("T,O,L", [(5, 128, 8192), (20, 130, 8208), (40, 100, 4096), (64, 513, 6160), (100, 300, 8192),
+                                   (200, 128, 4112), (333, 200, 9232)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_product_of_split_tiles(T, O, L, dt):
+    """Few tiles of long rows: K is divided among the CTAs of a cluster, up to eight."""
+    test_product_matches_exact_sums(T, O, L, dt)
