@@ -13,6 +13,7 @@ from . import _lib
 
 _DT = {torch.bfloat16: _lib.FQ_BF16, torch.float16: _lib.FQ_FP16}
 _OUT_DT = {**_DT, torch.float32: _lib.FQ_FP32}
+_INT_OUT = {"int32": _lib.FQ_OUT_INT32, "int8": _lib.FQ_OUT_INT8}  # else INT4
 
 
 def _stream_ptr(stream=None):
@@ -33,14 +34,14 @@ def _fits(t, dtype, device):
     return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
 
 
-def _empty(shape, dtype, device, stream):
-    """An output or a workspace that a call on `stream` (None: the current one) writes. It is
-    taken from that stream's memory: memory that another stream freed may still be read by what
-    is queued there."""
+def _empty(like, shape, dtype, stream):
+    """An output or a workspace, on the device of `like`, that a call on `stream` (None: the
+    current one) writes. It is taken from that stream's memory: memory that another stream freed
+    may still be read by what is queued there."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _ptr(t):
@@ -183,21 +184,23 @@ class FlatQuant:
         K, M, N = self.K, self.M, self.N
         if out is None:
             if out_dtype == "int8":
-                out = _empty((K, M * N), torch.int8, x.device, stream)
+                out = _empty(x, (K, M * N), torch.int8, stream)
             elif out_dtype == "int32":
-                out = _empty((K, M, N // 8), torch.int32, x.device, stream)
+                out = _empty(x, (K, M, N // 8), torch.int32, stream)
             else:
-                out = _empty((K, M * N // 2), torch.uint8, x.device, stream)
+                out = _empty(x, (K, M * N // 2), torch.uint8, stream)
         else:
             _check_output("out", out, K * M * N // (1 if out_dtype == "int8" else 2), x.device)
         if quant_scale is None:
-            quant_scale = _empty((K,), torch.float32, x.device, stream)
+            quant_scale = _empty(x, (K,), torch.float32, stream)
         else:
             _check_output("quant_scale", quant_scale, 4 * K, x.device, torch.float32)
-        fmt = {"int32": _lib.FQ_OUT_INT32, "int8": _lib.FQ_OUT_INT8}.get(out_dtype, _lib.FQ_OUT_INT4)
-        _lib.check(self._lib.fq_quantize_per_token(
-            self._h, x.data_ptr(), P1.data_ptr(), P2.data_ptr(), float(clip_ratio), fmt, out.data_ptr(),
-            quant_scale.data_ptr(), _raw_stream(stream, x.get_device())), "fq_quantize_per_token")
+        st = self._lib.fq_quantize_per_token(
+            self._h, x.data_ptr(), P1.data_ptr(), P2.data_ptr(), float(clip_ratio),
+            _INT_OUT.get(out_dtype, _lib.FQ_OUT_INT4), out.data_ptr(), quant_scale.data_ptr(),
+            _raw_stream(stream, x.get_device()))
+        if st != _lib.FQ_OK:
+            _lib.check(st, "fq_quantize_per_token")
         return out, quant_scale
 
     def quantize_mx(self, x, P1, P2, dst_type_max=0.0, out=None, scales=None, stream=None):
@@ -289,9 +292,8 @@ def int8_matmul(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stat
                             ("w_scale", w_scale, torch.float32)):
             _check_input(name, t, dt)
         _check_device(a, a_scale=a_scale, w=w, w_scale=w_scale)
-    for name, t, dims in (("a", a, 2), ("a_scale", a_scale, 1), ("w", w, 2), ("w_scale", w_scale, 1)):
-        if t.dim() != dims:
-            raise ValueError(f"{name} must have {dims} dimension{'s' if dims > 1 else ''}")
+    if (a.dim(), a_scale.dim(), w.dim(), w_scale.dim()) != (2, 1, 2, 1):
+        raise ValueError("a and w must have two dimensions, a_scale and w_scale one")
     if out_dtype not in _OUT_DT:
         raise ValueError("out_dtype must be torch.bfloat16, torch.float16 or torch.float32")
     T, L = a.shape
@@ -301,7 +303,7 @@ def int8_matmul(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stat
     if a_scale.numel() != T or w_scale.numel() != O:
         raise ValueError("a_scale and w_scale must have one scale per row of a and of w")
     if out is None:
-        out = _empty((T, O), out_dtype, a.device, stream)
+        out = _empty(a, (T, O), out_dtype, stream)
     else:
         _check_output("out", out, T * O * out_dtype.itemsize, a.device, out_dtype)
     if status is not None:
@@ -362,6 +364,7 @@ class KVCache:
         self._lib = _lib.load()
         self._desc = _lib.KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                       self.num_pages, self.kv_heads, self.page_size, self.head_dim)
+        self._desc_ref = ctypes.byref(self._desc)
         self._workspace_bytes = {}  # by the sizes that decide it
 
     k = property(lambda self: self._tensors[0], doc="E4M3 codes of the keys")
@@ -440,14 +443,14 @@ class KVCache:
             qs = self._tokens("q", q, T, None, k.dtype)
             hq = q.shape[1]
             if q_out is None:
-                q_out = _empty((T, hq, self.head_dim), q.dtype, q.device, stream)
+                q_out = _empty(q, (T, hq, self.head_dim), q.dtype, stream)
             else:
                 _check_output("q_out", q_out, T * hq * self.head_dim * 2, q.device, q.dtype)
             q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             raise ValueError("q_out needs q")
         st = self._lib.fq_kv_append(
-            ctypes.byref(self._desc), ctypes.byref(batch), T, _DT[k.dtype], k.data_ptr(), ks, v.data_ptr(), vs, freq,
+            self._desc_ref, ctypes.byref(batch), T, _DT[k.dtype], k.data_ptr(), ks, v.data_ptr(), vs, freq,
             rot, 1 if interleaved else 0, q_ptr, qs, hq, out_ptr, self._status_ptr, _raw_stream(stream, self._device))
         if st != _lib.FQ_OK:
             _lib.check(st, "fq_kv_append")
@@ -469,26 +472,26 @@ class KVCache:
         if max_seq_len is None:
             max_seq_len = batch.table_width * self.page_size
         if out is None:
-            out = _empty((T, hq, D), q.dtype, q.device, stream)
+            out = _empty(q, (T, hq, D), q.dtype, stream)
         else:
             _check_output("out", out, T * hq * D * 2, q.device, q.dtype)
         if lse is not None:
             _check_output("lse", lse, T * hq * 4, q.device, torch.float32)
         elif return_lse:
-            lse = _empty((T, hq), torch.float32, q.device, stream)
+            lse = _empty(q, (T, hq), torch.float32, stream)
         sizes = (T, hq, batch.num_seqs, batch.table_width, max_q_len, max_seq_len)
         need = self._workspace_bytes.get(sizes)
         if need is None:
             n = ctypes.c_int64(0)
-            _lib.check(self._lib.fq_kv_attention_workspace(ctypes.byref(self._desc), ctypes.byref(batch), T, hq,
+            _lib.check(self._lib.fq_kv_attention_workspace(self._desc_ref, ctypes.byref(batch), T, hq,
                                                            int(max_q_len), int(max_seq_len), ctypes.byref(n)),
                        "fq_kv_attention_workspace")
             if len(self._workspace_bytes) >= 4096:
                 self._workspace_bytes.clear()
             need = self._workspace_bytes[sizes] = n.value
-        ws = _empty(need, torch.uint8, q.device, stream) if need else None
+        ws = _empty(q, (need,), torch.uint8, stream) if need else None
         st = self._lib.fq_kv_attention(
-            ctypes.byref(self._desc), ctypes.byref(batch), T, _DT[q.dtype], q.data_ptr(), qs, hq, int(max_q_len),
+            self._desc_ref, ctypes.byref(batch), T, _DT[q.dtype], q.data_ptr(), qs, hq, int(max_q_len),
             int(max_seq_len), float(scale if scale is not None else D ** -0.5), 1 if causal else 0, out.data_ptr(),
             lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None, need,
             self._status_ptr, _raw_stream(stream, self._device))
