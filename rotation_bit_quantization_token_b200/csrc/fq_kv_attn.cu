@@ -176,7 +176,11 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   int* s_page = reinterpret_cast<int*>(sh + 1);
   uint16_t* s_scale = reinterpret_cast<uint16_t*>(s_page + (p.chunk >> ps_log) + 1);
   const int n_pages = (keys + ps - 1) >> ps_log;
-  if (tid < kWarps * G_::kStages) mbar_init(&sh->full[tid / G_::kStages][tid % G_::kStages], 1);
+  if (tid < kWarps * G_::kStages) {
+    mbar_init(&sh->full[tid / G_::kStages][tid % G_::kStages], 1);
+    fence_barrier_init();
+    fence_proxy_async();
+  }
   if (tid == 0) sh->abort = 0;
   const int* table = p.b.page_table + int64_t(b) * p.b.table_width + (c0 >> ps_log);
   for (int i = tid; i < n_pages; i += kThreads) {
@@ -186,10 +190,6 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       if (p.status != nullptr) atomicOr(p.status, FQ_KV_BAD_BATCH);
     }
     s_page[i] = pg;
-  }
-  if (tid == 0) {
-    fence_barrier_init();
-    fence_proxy_async();
   }
   __syncthreads();
 
@@ -296,9 +296,23 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   int unit = 0;        // exponent of the output's current unit
   bool first_unit = true;
 
-  int stage = 0, phase = 0;
+  int stage = 0, phase = 0, in_flight = 0;
   for (int w = warp; w < n_tiles; w += kWarps) {
-    if (!warp_wait(&sh->full[warp][stage], uint32_t(phase), &sh->abort, p.status, kStFull)) break;
+    if (!warp_wait(&sh->full[warp][stage], uint32_t(phase), &sh->abort, p.status, kStFull)) {
+      // this warp's loads in flight land before its memory is used again (or a limit)
+      for (; w < n_tiles && lane == 0; w += kWarps) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(smem_u32(&sh->full[warp][stage]), uint32_t(phase)) && globaltimer() - t0 < kTimeoutNs / 4) {
+        }
+        if (++stage == G_::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (++in_flight == G_::kStages) break;
+      }
+      __syncwarp();
+      break;
+    }
     const uint32_t kbase = ring + uint32_t(stage * G_::kStageBytes), vbase = kbase + G_::kTileBytes;
     const int k0 = w * kTK;
     if (k0 + kTK > keys || missing) {
