@@ -49,10 +49,10 @@ struct Geo {
   static constexpr int kStage = kWBytes + kABytes;
   // two CTAs per SM for the narrow tiles (about 100 KB each in flight), one for the wide ones
   static constexpr int kMinBlocks = kBT <= 64 ? 2 : 1;
-  static constexpr int kStages = kBT <= 16 ? 5 : (kBT <= 32 ? 4 : (kBT == 64 ? (kSplit ? 3 : 4) : (kBT == 128 ? (kSplit ? 4 : 5) : (kSplit ? 3 : 4))));
-  static constexpr int kMaxSplit = kBT == 256 ? 2 : (kBT == 64 ? 4 : 8);  // as the partial sums fit
+  static constexpr int kStages = kBT <= 16 ? 5 : (kBT <= 32 ? 4 : (kBT == 64 ? (kSplit ? 3 : 4) : (kBT <= 192 ? (kSplit ? 4 : 5) : (kSplit ? 3 : 4))));
+  static constexpr int kMaxSplit = kBT >= 192 ? 2 : (kBT == 64 ? 4 : 8);  // as the partial sums fit
   static constexpr int kBufs = kSplit ? 1 : 2;  // accumulators
-  static constexpr uint32_t kCols = kBufs * kBT < 32 ? 32u : uint32_t(kBufs * kBT);
+  static constexpr uint32_t kCols = kBufs * kBT < 32 ? 32u : uint32_t(kBufs * (kBT == 192 ? 256 : kBT));  // a power of two
   // partial sums from the other CTAs of the cluster, [sender][channel][token of this CTA's share]; a
   // channel's row is 16 bytes longer than its tokens, so that neighbouring lanes read other banks
   static constexpr int in_bytes(int split) { return (split - 1) * kBO * (kBT / split + 4) * 4; }
@@ -302,18 +302,30 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
           // of integers is exact in any order); then this CTA's own share is completed and stored. No
           // CTA reads another's memory, so each may leave when it is done: two cluster barriers around
           // remote reads took 4000 clocks more.
-          const int per_log = 31 - __clz(per);
+          constexpr bool kHalves = G::kMaxSplit == 2;  // shares of whole chunks, of any size
+          static_assert(!kHalves || kBT % (2 * kChunk) == 0, "shares");
+          const int per_log = kHalves ? 31 : 31 - __clz(per);
           const int ch = q * 32 + lane;
           const uint32_t in_base = sbase + G::kOffIn, in_bar = smem_u32(&bars->in_full);
 #pragma unroll 1
           for (int c = 0; c < kBT / kChunk; ++c) {
-            if ((c * kChunk) >> per_log == rank && (c * kChunk + kChunk - 1) >> per_log == rank) continue;
+            if constexpr (kHalves) {
+              if ((c * kChunk >= kBT / 2) == rank) continue;
+            } else {
+              if ((c * kChunk) >> per_log == rank && (c * kChunk + kChunk - 1) >> per_log == rank) continue;
+            }
             uint32_t r[kChunk];
             const uint32_t t_col = t_lane + uint32_t(c * kChunk);
             if constexpr (kChunk == 16) tmem_ld16(t_col, r);
             else tmem_ld32(t_col, r);
             tmem_wait_ld();
-            if (per_log >= 2) {
+            if constexpr (kHalves) {
+              // one remote address for the chunk (one for every four tokens: 333 x 4099 x 8192 26 us for 21)
+              const int at = (ch * (kBT / 2 + 4) + c * kChunk - (1 - rank) * (kBT / 2)) * 4;
+              const uint32_t to = remote_addr(in_base + uint32_t(at), uint32_t(1 - rank)), bar = remote_addr(in_bar, uint32_t(1 - rank));
+#pragma unroll
+              for (int e = 0; e < kChunk; e += 4) push4(to + uint32_t(e * 4), r + e, bar);
+            } else if (per_log >= 2) {
 #pragma unroll
               for (int e = 0; e < kChunk; e += 4) {
                 const int t = c * kChunk + e, dest = t >> per_log;
@@ -348,7 +360,7 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
               if (per_log >= 2) {
 #pragma unroll
                 for (int e = 0; e < kChunk; e += 4) {
-                  if ((c * kChunk + e) >> per_log != rank) continue;
+                  if (!kHalves && (c * kChunk + e) >> per_log != rank) continue;
                   const int4 v = *reinterpret_cast<const int4*>(in + c * kChunk + e);
                   r[e] += uint32_t(v.x);
                   r[e + 1] += uint32_t(v.y);
@@ -369,7 +381,7 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 #pragma unroll
             for (int e = 0; e < kChunk; ++e, dst += p.O) {
               const float f = float(int(r[e])) * __shfl_sync(0xffffffffu, as, e) * ws;
-              if (there && (c * kChunk + e) >> per_log == rank && tc + e < p.T) *dst = to_out<Out>(f);
+              if (there && (kHalves || (c * kChunk + e) >> per_log == rank) && tc + e < p.T) *dst = to_out<Out>(f);
             }
           }
         } else {
@@ -655,8 +667,8 @@ cudaError_t launch_tile(const I8GemmParams& g, int num_sms, cudaStream_t stream)
   // Split K while that takes no SM a second CTA (1 x 14336 x 4096, 112 tiles: whole 14.5 us, in two
   // 15.4; 1 x 4096 x 4096, 32 tiles: whole 13.2, in four 8.5, in eight 10.3) and as long as each CTA keeps
   // four stages of work (4 x 2048 x 2048: 5.8 us with four, 6.6 with eight), or eight where the partial
-  // sums are 128 KB (300 x 1024 x 1024: whole 9.9 us, in two 11.2).
-  constexpr int kLeast = kBT == 256 ? 8 : 4;
+  // sums are 96 KB or more (300 x 1024 x 1024: whole 8.7 us, in two 9.2; 512 x 1024 x 1024 9.9 and 11.0).
+  constexpr int kLeast = kBT >= 192 ? 8 : 4;
   int split = 1;
   while (split < G::kMaxSplit && tiles * split * 2 <= num_sms && nk >= split * 2 * kLeast) split *= 2;
   return split > 1 ? launch_t<kBT, Out, true>(g, split, num_sms, stream) : launch_t<kBT, Out, false>(g, 1, num_sms, stream);
@@ -670,11 +682,15 @@ cudaError_t launch_out(const I8GemmParams& g, int num_sms, cudaStream_t stream) 
   if (g.T <= 32) return launch_tile<32, Out>(g, num_sms, stream);
   if (g.T <= 64) return launch_tile<64, Out>(g, num_sms, stream);
   if (g.T <= 128) return launch_tile<128, Out>(g, num_sms, stream);
-  // Pairs where their tiles come close to filling the machine: 1024 x 6144 x 4096 (96 tiles) 28.5 us, 32.4
-  // with tiles of one CTA; 1024 x 4096 x 4096 (64) 19.3 and 20.5; 768 x 4096 x 4096 (48 tiles) 19.0 and
-  // 20.0, but 333 x 4099 x 8192 (34) 26.5 and 25.4, split.
+  // Pairs where their tiles take half of the machine or more (tiles of one CTA are then too many to be
+  // split): 512 x 5120 x 14336 (40 tiles) 42.3 us, 51.8 with tiles of one CTA; 512 x 6144 x 4096 (48)
+  // 19.0 and 20.3; 1024 x 6144 x 4096 (96) 28.5 and 32.4; with short rows 768 x 4096 x 1024 11.8 and 11.2.
+  // Below it 333 x 4099 x 8192 (34) 26.5 and 21.4, split.
   const int64_t pairs = ((g.O + kPairO - 1) / kPairO) * ((g.T + kPairT - 1) / kPairT);
-  if (pairs * 10 >= int64_t(num_sms / 2) * 7) return launch_pair<Out>(g, num_sms, stream);
+  if (pairs * 2 >= int64_t(num_sms / 2)) return launch_pair<Out>(g, num_sms, stream);
+  // 192 token columns where that pads less than 256: 333 x 4099 x 8192 21.4 us for 25, 384 x 4096 x 14336
+  // 30.1 for 36
+  if ((g.T + 191) / 192 * 192 < (g.T + 255) / 256 * 256) return launch_tile<192, Out>(g, num_sms, stream);
   return launch_tile<256, Out>(g, num_sms, stream);
 }
 

@@ -244,3 +244,10 @@ def test_rotated_linear_layer(K, M, N, O):
 def test_product_of_split_tiles(T, O, L, dt):
     """Few tiles of long rows: K is divided among the CTAs of a cluster, up to eight."""
     test_product_matches_exact_sums(T, O, L, dt)
+
+
+@pytest.mark.parametrize("T,O,L", [(130, 100, 1040), (192, 257, 4112), (333, 300, 8192), (384, 6200, 528), (570, 129, 2064)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_product_of_middle_tiles(T, O, L, dt):
+    """Token counts that pad less in tiles of 192, whole and split."""
+    test_product_matches_exact_sums(T, O, L, dt)
