@@ -20,7 +20,8 @@
 // loading 128 rows of both operands, 32 KB a stage instead of 48 for the same products. The single
 // kernel runs at 757 clocks a stage there (63 bytes a clock and SM, what L2 delivers), where the
 // MMAs need 512.
-// Every wait is bounded; on expiry the kernel sets a bit in the caller's status word.
+// 8192 x 4096 x 14336: 303 us, 3.2 POP/s in bursts (363 us repeated, at 1000 W); 1 x 14336 x 4096:
+// 14.9 us, 3.9 TB/s. Every wait is bounded; on expiry the kernel sets a bit in the caller's status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -3,7 +3,8 @@
 // Rows are (new token, query head) pairs that share one key / value head (row r of a sequence: token
 // r / G, head r % G of the group, G = q_heads / kv_heads), 8 or 16 of them per CTA, so a decode step
 // reads each cached byte once for the whole group. The kernel is bound by reading the cache: 2 D
-// bytes a token and head.
+// bytes a token and head: 64 sequences of 500-16000 tokens, 8 heads of 128, take 172 us, 6.0 TB/s; one
+// of 700 tokens takes 7.6 us, which is launch and latency.
 //
 // One CTA takes its rows and one chunk of keys; its four warps take tiles of 4096 / D keys in turn,
 // each through a ring of its own (TMA boxes of 128-byte rows, swizzled; no barrier between the
@@ -730,6 +731,8 @@ cudaError_t launch_attn(const KvAttnParams& p, const KvAttnPlan& plan, cudaStrea
     // beside prompts that are not split, only the few rows of the other sequences can be
     const int few = plan.tc_row_tiles > 0 && plan.tc_splits == 1 ? plan.row_tiles * plan.tile_rows : 0;
     const int64_t rows = few > 0 ? int64_t(p.b.num_seqs) * p.c.kv_heads * few : p.T * p.q_heads;
+    // a row each where there are many chunks: one sequence of 65536 33 us, 52 with four rows a CTA; but
+    // with 4 chunks of 64 sequences (6000 tokens) 133 us, 137.5 with a row each
     const bool wide = p.ws_splits > 8;
     const int64_t blocks = wide ? rows : (rows + kThreads / (D / 4) - 1) / (kThreads / (D / 4));
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
@@ -767,6 +770,8 @@ KvAttnPlan plan_kv_attn(const fq_kv_cache& c, const fq_kv_batch& b, int64_t T, i
   plan.tc_rows = 64;
   const int64_t few = b.num_seqs == 1 && rows > plan.tc_rows ? 0 : (rows < plan.tc_rows ? rows : plan.tc_rows);
   if (few == 0) plan.tc_rows = 0;  // one sequence: whatever its length, one kernel
+  // 8 rows where that is all: 64 sequences of 6000, 8 rows, 133 us, 160 in CTAs of 16 rows; 16 sequences
+  // of 4000, 16 rows, 35 us, 42.5 in CTAs of 8, which read the cache twice
   plan.tile_rows = few <= 8 ? 8 : 16;
   plan.row_tiles = int((few + plan.tile_rows - 1) / plan.tile_rows);
   plan.splits = plan.tc_splits = 1;
