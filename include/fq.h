@@ -232,7 +232,8 @@ typedef struct {
  *               formed and reduced in float64, the rotation in float32. rot_dim a multiple of 16,
  *               at most head_dim
  *   q, q_out    [T, q_heads, head_dim] (q tokens q_stride apart, q_out contiguous): the queries,
- *               rotated alike and rounded once to dtype; both NULL with q_heads = 0
+ *               rotated alike and rounded once to dtype (q_out may be q where q is contiguous);
+ *               both NULL with q_heads = 0
  * A page that already holds tokens of the sequence keeps the larger of its exponent and the new
  * tokens'; when it grows, the codes of the older tokens are rounded once more (exact but for
  * codes that become subnormal). Rows that belong to no token are not written. The pages that

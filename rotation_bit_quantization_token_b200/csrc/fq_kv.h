@@ -33,7 +33,7 @@ struct KvAttnParams {
   const void* q;
   void* out;
   float* lse;
-  float* ws;         // partial results: [T * q_heads, splits, head_dim + 2]
+  float* ws;         // partial results: [T * q_heads, ws_splits, head_dim + 4]
   uint32_t* status;
   int64_t T, q_stride, max_seq_len;
   int q_heads, max_q_len, causal, fp16;

@@ -651,3 +651,48 @@ def test_attention_chunk_with_a_page_outside():
     assert np.allclose(f64(lse[0]), np.log(np.exp(z).sum(-1)), atol=1e-5)
     p = np.exp(z) / np.exp(z).sum(-1, keepdims=True)
     assert np.allclose(f64(out[0]), p @ v[keep], rtol=2.0 ** -7, atol=2e-3)
+
+
+@pytest.mark.parametrize("new,ctx,longest", [([1, 1, 2], [1500, 700, 90], 1600), ([40, 1, 30], [900, 2500, 0], 2600)])
+def test_graphs_replayed_with_other_lengths(new, ctx, longest):
+    """Two graphs of one cache (chunks joined in clusters; a prompt and decode steps in one call)
+    replayed at the same time with other lengths and pages, and a third call beside them."""
+    s = Setup(new, ctx, H=2, D=128, page=32, seed=64, width=-(-longest // 32)).fill()
+    cache = s.cache()
+    cu, lens, table = s.batch()
+    q = torch.randn(sum(new), 8, 128, device="cuda").to(torch.bfloat16)
+    call = lambda: cache.attention(q, cu, lens, table, max(new), max_seq_len=longest, return_lse=True)  # noqa: E731
+    call()
+    graphs, outs = [], []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(call())
+        graphs.append(gr)
+    lens.copy_(_i32([n + c // 3 for n, c in zip(new, ctx)]))
+    table.copy_(table[:, torch.arange(table.shape[1] - 1, -1, -1)].clone().clamp_(min=0))
+    want = call()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for gr, x in zip(graphs, streams):
+            with torch.cuda.stream(x):
+                gr.replay()
+        again = call()
+    torch.cuda.synchronize()
+    assert cache.device_status() == 0
+    bits = lambda x: x.view(torch.uint8)  # noqa: E731  (the turned tables reach NaN codes)
+    for o, l in outs + [again]:
+        assert torch.equal(bits(o), bits(want[0])) and torch.equal(bits(l), bits(want[1]))
+
+
+def test_append_in_place_of_the_queries():
+    """q_out may be q itself."""
+    s = Setup([3, 40], [5, 0], H=2, D=64, page=16, seed=65)
+    cu, lens, table = s.batch()
+    k = torch.randn(43, 2, 64, device="cuda").half()
+    q = torch.randn(43, 12, 64, device="cuda").half()
+    f = torch.rand(32, device="cuda")
+    want = s.cache().append(k, k, cu, lens, table, q=q, inv_freq=f)
+    got = s.cache().append(k, k, cu, lens, table, q=q, inv_freq=f, q_out=q)
+    assert got is q and torch.equal(got, want)
