@@ -240,8 +240,9 @@ typedef struct {
  * receive tokens are distinct, in one sequence and between sequences: two appends to one page
  * race (attention may share pages).
  *   status      a device word, or NULL
- * Strides are multiples of 8 elements, pointers 16-byte aligned. Allocates nothing;
- * asynchronous on stream; deterministic. Errors: FQ_ERR_NULLPTR, FQ_ERR_INVALID, FQ_ERR_CUDA. */
+ * Strides are multiples of 8 elements, pointers 16-byte aligned (inv_freq and status 4-byte).
+ * Allocates nothing; asynchronous on stream; deterministic. Errors: FQ_ERR_NULLPTR, FQ_ERR_INVALID,
+ * FQ_ERR_CUDA. */
 FQ_API fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch, int64_t T, fq_dtype dtype,
                               const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                               const float *inv_freq, int32_t rot_dim, int interleaved,

@@ -164,8 +164,8 @@ __device__ __forceinline__ void rotate_queries(const KvAppendParams& p, int64_t 
   if (t < t_first || t >= t_end || t_first < 0 || t_end > p.T || len < t_end - t_first) return;  // no sequence's token
   float4 cs = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
   if (z.turned) {
-    const float2 f = *reinterpret_cast<const float2*>(p.inv_freq + 2 * lq);
-    const float2 a = cos_sin_of(pos, f.x), c = cos_sin_of(pos, f.y);
+    // (one at a time: inv_freq is aligned to its elements only)
+    const float2 a = cos_sin_of(pos, __ldg(p.inv_freq + 2 * lq)), c = cos_sin_of(pos, __ldg(p.inv_freq + 2 * lq + 1));
     cs = make_float4(a.x, a.y, c.x, c.y);
   }
 #pragma unroll
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, kSteps == 8 ? 4 : 2)
 kv_append_kernel(const KvAppendParams p, const unsigned kv_ctas, const unsigned groups) {
   constexpr int kLpr = D / 4, kRps = 32 / kLpr;  // lanes per row, rows per step of a warp
   constexpr int kWarpRows = kSteps * kRps;
-  extern __shared__ float2 s_cs[];  // [rows][rot / 2]
+  extern __shared__ __align__(16) float2 s_cs[];  // [rows][rot / 2], read two at a time
   __shared__ float s_max[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (blockIdx.x >= kv_ctas) {
