@@ -177,6 +177,13 @@ FQ_API fq_status fq_int8_matmul(int64_t T, int64_t O, int64_t L, const int8_t* a
                                 const int8_t* w, const float* w_scale, fq_dtype out_type, void* C,
                                 uint32_t* status, struct CUstream_st* stream);
 
+/* Test hook for the failure path of fq_int8_matmul: process-wide and one-shot, like
+ * fq_static_debug_arm_stall. In the next call one CTA of every cluster (every CTA where none is
+ * formed) issues no loads, and every bounded wait has a limit of wait_limit_s seconds
+ * (0 < wait_limit_s <= 10): the waits run out, the kernel sets the status word and returns; the
+ * outputs of that call are undefined. Returns FQ_ERR_INVALID for a limit out of range. */
+FQ_API fq_status fq_int8_debug_arm_stall(double wait_limit_s);
+
 /* Paged key / value cache held in 8 bits (an addition of this library, like everything that
  * takes an fq_kv_cache). A page holds page_size consecutive tokens of one sequence. The
  * values of one page and one head share one power of two, kept as an E8M0 byte like the

@@ -7,6 +7,7 @@
 // parameter table and error-code table.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -32,6 +33,9 @@ struct fq_handle {
 namespace {
 
 thread_local int g_last_cuda_error = 0;
+
+// One-shot test hook (fq_int8_debug_arm_stall): 0 = off, else the wait limit in ns.
+std::atomic<uint64_t> g_int8_stall_ns{0};
 
 fq_status cuda_fail(cudaError_t e) {
   g_last_cuda_error = int(e);
@@ -224,9 +228,15 @@ fq_status fq_int8_matmul(int64_t T, int64_t O, int64_t L, const int8_t* a, const
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e);
-  fq::I8GemmParams p{a, a_scale, w, w_scale, C, status, T, O, L, out_type};
+  fq::I8GemmParams p{a, a_scale, w, w_scale, C, status, T, O, L, out_type, g_int8_stall_ns.exchange(0)};
   e = fq::launch_i8gemm(p, sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FQ_OK : cuda_fail(e);
+}
+
+fq_status fq_int8_debug_arm_stall(double wait_limit_s) {
+  if (!(wait_limit_s > 0.0 && wait_limit_s <= 10.0)) return FQ_ERR_INVALID;
+  g_int8_stall_ns.store(uint64_t(wait_limit_s * 1e9));
+  return FQ_OK;
 }
 
 fq_status fq_set_kernel(fq_handle* h, fq_kernel kernel) {

@@ -82,6 +82,8 @@ struct Params {
   int64_t T, O;
   int tiles_o, num_tiles, nk, split;
   int vec;  // rows of C are 16-byte aligned
+  int stall;          // test hook: see fq_int8_debug_arm_stall
+  uint64_t limit_ns;  // of every bounded wait
 };
 
 template <typename Out>
@@ -178,7 +180,8 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     tma_load_2d(dst + G::kWBytes, &map_a, kb * kBK, (tile / p.tiles_o) * kBT, &bars->full[s]);
   };
   // the first round of loads goes out before the CTA has met: nothing else writes the ring
-  const int n_early = n_local > 0 ? min(k1 - k0, G::kStages) : 0;
+  const bool stall = p.stall != 0 && rank == 0;  // (test hook) this CTA issues no loads
+  const int n_early = n_local > 0 && !stall ? min(k1 - k0, G::kStages) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < G::kStages; ++s) {
@@ -213,11 +216,11 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     if (lane == 0) {
       int it = n_early;
       bool ok = true;
-      for (int i = 0; ok && i < n_local; ++i) {
+      for (int i = 0; ok && !stall && i < n_local; ++i) {
         for (int kb = k0 + (i == 0 ? n_early : 0); kb < k1; ++kb, ++it) {
           const int s = it % G::kStages;
           if (it >= G::kStages &&
-              !wait_bounded(&bars->empty[s], ((it / G::kStages) - 1) & 1, &bars->abort, p.status, kStEmpty)) {
+              !wait_bounded(&bars->empty[s], ((it / G::kStages) - 1) & 1, &bars->abort, p.status, kStEmpty, p.limit_ns)) {
             ok = false;
             break;
           }
@@ -229,7 +232,7 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         const uint32_t b = smem_u32(&bars->full[j % G::kStages]);
         const uint64_t tz = globaltimer();
         while (!mbar_try_wait(b, (j / G::kStages) & 1)) {
-          if (globaltimer() - tz > kTimeoutNs) {
+          if (globaltimer() - tz > p.limit_ns) {
             if (p.status != nullptr) atomicOr(p.status, kStDrain);
             break;
           }
@@ -243,11 +246,11 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     bool ok = true;
     for (int i = 0; ok && i < n_local; ++i) {
       const int buf = i & 1;
-      if (i >= 2 && !warp_wait(&bars->d_empty[buf], ((i >> 1) - 1) & 1, &bars->abort, p.status, kStDEmpty)) break;
+      if (i >= 2 && !warp_wait(&bars->d_empty[buf], ((i >> 1) - 1) & 1, &bars->abort, p.status, kStDEmpty, p.limit_ns)) break;
       tc_fence_after();
       for (int kb = k0; kb < k1; ++kb, ++it) {
         const int s = it % G::kStages;
-        if (!warp_wait(&bars->full[s], (it / G::kStages) & 1, &bars->abort, p.status, kStFull)) {
+        if (!warp_wait(&bars->full[s], (it / G::kStages) & 1, &bars->abort, p.status, kStFull, p.limit_ns)) {
           ok = false;
           break;
         }
@@ -274,7 +277,7 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         const uint32_t b = smem_u32(&bars->empty[j % G::kStages]);
         const uint64_t tz = globaltimer();
         while (!mbar_try_wait(b, (j / G::kStages) & 1)) {
-          if (globaltimer() - tz > kTimeoutNs) {
+          if (globaltimer() - tz > p.limit_ns) {
             if (p.status != nullptr) atomicOr(p.status, kStDrain);
             break;
           }
@@ -291,7 +294,7 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       const int buf = i & 1;
       const int64_t o = int64_t(tile % p.tiles_o) * kBO + q * 32 + lane;
       const int64_t t0 = int64_t(tile / p.tiles_o) * kBT;
-      const bool ok = warp_wait(&bars->d_full[buf], (i >> 1) & 1, &bars->abort, p.status, kStDFull);
+      const bool ok = warp_wait(&bars->d_full[buf], (i >> 1) & 1, &bars->abort, p.status, kStDFull, p.limit_ns);
       if (ok) {
         tc_fence_after();
         const float ws = o < p.O ? __ldg(p.w_scale + o) : 0.0f;
@@ -346,7 +349,7 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
               }
             }
           }
-          if (!warp_wait(&bars->in_full, 0, &bars->abort, p.status, kStIn)) break;
+          if (!warp_wait(&bars->in_full, 0, &bars->abort, p.status, kStIn, p.limit_ns)) break;
 #pragma unroll 1
           for (int c = rank * per / kChunk; c * kChunk < (rank + 1) * per; ++c) {
             uint32_t r[kChunk];
@@ -411,6 +414,19 @@ i8gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tmem, G::kCols);
   }
+  if constexpr (kSplit) {
+    // A CTA that gave up may still be sent partial sums: it stays until the others have sent theirs
+    // (or have left, which counts as arriving) and what is on its way has landed, or a limit. One
+    // that did not give up has waited for all of its own.
+    if (*reinterpret_cast<volatile int*>(&bars->abort) != 0) {
+      cluster_sync();
+      if (threadIdx.x == 0) {
+        const uint64_t tz = globaltimer();
+        while (!mbar_try_wait(smem_u32(&bars->in_full), 0) && globaltimer() - tz < p.limit_ns) {
+        }
+      }
+    }
+  }
 }
 
 template <typename Out>
@@ -424,6 +440,8 @@ Params params_of(const I8GemmParams& g) {
   p.O = g.O;
   p.nk = int((g.L + kBK - 1) / kBK);
   p.vec = (reinterpret_cast<uintptr_t>(g.C) & 15u) == 0 && (g.O * int64_t(sizeof(Out))) % 16 == 0;
+  p.stall = g.stall_ns != 0;
+  p.limit_ns = g.stall_ns != 0 ? g.stall_ns : kTimeoutNs;
   return p;
 }
 
@@ -505,7 +523,7 @@ i8gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         for (int kb = 0; kb < p.nk; ++kb, ++it) {
           const int s = it % kPairStages;
           if (it >= kPairStages &&
-              !wait_bounded(&bars->empty[s], ((it / kPairStages) - 1) & 1, &bars->abort, p.status, kStEmpty)) {
+              !wait_bounded(&bars->empty[s], ((it / kPairStages) - 1) & 1, &bars->abort, p.status, kStEmpty, p.limit_ns)) {
             ok = false;
             break;
           }
@@ -525,11 +543,11 @@ i8gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     bool ok = true;
     for (int i = 0; ok && i < n_local; ++i) {
       const int buf = i & 1;
-      if (i >= 2 && !warp_wait(&bars->d_empty[buf], ((i >> 1) - 1) & 1, &bars->abort, p.status, kStDEmpty)) break;
+      if (i >= 2 && !warp_wait(&bars->d_empty[buf], ((i >> 1) - 1) & 1, &bars->abort, p.status, kStDEmpty, p.limit_ns)) break;
       tc_fence_after();
       for (int kb = 0; kb < p.nk; ++kb, ++it) {
         const int s = it % kPairStages;
-        if (!warp_wait(&bars->full[s], (it / kPairStages) & 1, &bars->abort, p.status, kStFull)) {
+        if (!warp_wait(&bars->full[s], (it / kPairStages) & 1, &bars->abort, p.status, kStFull, p.limit_ns)) {
           ok = false;
           break;
         }
@@ -554,7 +572,7 @@ i8gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         const uint32_t b = smem_u32(&bars->empty[j % kPairStages]);
         const uint64_t tz = globaltimer();
         while (!mbar_try_wait(b, (j / kPairStages) & 1)) {
-          if (globaltimer() - tz > kTimeoutNs) {
+          if (globaltimer() - tz > p.limit_ns) {
             if (p.status != nullptr) atomicOr(p.status, kStDrain);
             break;
           }
@@ -571,7 +589,7 @@ i8gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       const int buf = i & 1;
       const int64_t o0 = int64_t(tile % p.tiles_o) * kPairO + int64_t(rank) * kBO + q * 32;
       const int64_t t0 = int64_t(tile / p.tiles_o) * kPairT;
-      const bool ok = warp_wait(&bars->d_full[buf], (i >> 1) & 1, &bars->abort, p.status, kStDFull);
+      const bool ok = warp_wait(&bars->d_full[buf], (i >> 1) & 1, &bars->abort, p.status, kStDFull, p.limit_ns);
       if (ok) {
         tc_fence_after();
         const float ws = o0 + lane < p.O ? __ldg(p.w_scale + o0 + lane) : 0.0f;

@@ -81,6 +81,7 @@ struct I8GemmParams {
   uint32_t* status;      // bounded-wait status word, or nullptr
   int64_t T, O, L;
   fq_dtype out_type;
+  uint64_t stall_ns;     // test hook (fq_int8_debug_arm_stall): 0 = off, else the wait limit
 };
 cudaError_t launch_i8gemm(const I8GemmParams& p, int num_sms, cudaStream_t stream);
 

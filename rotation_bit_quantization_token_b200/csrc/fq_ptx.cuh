@@ -83,7 +83,7 @@ __device__ __forceinline__ void named_bar(int id, int count) {
 // a status bit and returns false. The clock is read once in 64 tries: reading it takes longer
 // than most waits here last, and a phase that completes meanwhile would be seen late.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, int* abort, uint32_t* status,
-                                             uint32_t code) {
+                                             uint32_t code, uint64_t limit_ns = kTimeoutNs) {
   const uint32_t b = smem_u32(bar);
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
@@ -92,7 +92,7 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, int
     if (*reinterpret_cast<volatile int*>(abort)) return false;
     const uint64_t now = globaltimer();
     if (t0 == 0) t0 = now;
-    if (now - t0 > kTimeoutNs) {
+    if (now - t0 > limit_ns) {
       *reinterpret_cast<volatile int*>(abort) = 1;
       if (status != nullptr) atomicOr(status, code);
       return false;
@@ -100,8 +100,8 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, int
   }
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, uint32_t* status,
-                                          uint32_t code) {
-  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort, status, code));
+                                          uint32_t code, uint64_t limit_ns = kTimeoutNs) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort, status, code, limit_ns));
 }
 
 // Shared-memory descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
