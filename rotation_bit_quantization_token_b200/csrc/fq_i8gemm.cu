@@ -72,6 +72,8 @@ struct Bars {
   uint64_t in_full;  // the other CTAs' partial sums are there
   uint32_t tmem_base;
   int abort;
+  int issued;                    // pairs: stages that this CTA's producer has loaded
+  int other_abort, other_issued;  // pairs: the other CTA's at its end
 };
 
 struct Params {
@@ -467,6 +469,9 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, 
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+__device__ __forceinline__ void st_cluster(uint32_t dst, int v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+}
 // arrives at the barrier's place in both CTAs of the pair
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {
   asm volatile(
@@ -516,7 +521,7 @@ i8gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   if (warp == kWarpProducer) {
     if (lane == 0) {
       int it = 0;
-      bool ok = true;
+      bool ok = p.stall == 0 || rank == 0;  // (test hook) the second CTA issues no loads
       for (int i = 0; ok && i < n_local; ++i) {
         const int tile = first + i * step;
         const int o0 = (tile % p.tiles_o) * kPairO + int(rank) * kBO, t0 = (tile / p.tiles_o) * kPairT + int(rank) * kBO;
@@ -535,6 +540,7 @@ i8gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           tma_load_pair(dst + kPairStage / 2, &map_a, kb * kBK, t0, bar);
         }
       }
+      bars->issued = it;
     }
     __syncwarp();
   } else if (warp == kWarpMma && rank == 0) {
@@ -611,7 +617,28 @@ i8gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) {  // how this CTA ended, for the other one
+    st_cluster(remote_addr(smem_u32(&bars->other_abort), rank ^ 1u), bars->abort);
+    st_cluster(remote_addr(smem_u32(&bars->other_issued), rank ^ 1u), bars->issued);
+  }
   cluster_sync();  // neither leaves while the other's MMAs or arrivals may reach it
+  if (bars->abort != 0 || bars->other_abort != 0) {
+    // One of them gave up, so loads may be in flight (in a call that is in order every stage has been
+    // multiplied). Both CTAs' loads are counted by the first one's barriers: it waits for the last
+    // stages, or a limit, arming those that only the second CTA has loaded; then both leave.
+    if (rank == 0 && threadIdx.x == 0) {
+      for (int j = bars->issued; j < bars->other_issued; ++j)
+        mbar_arrive_expect_tx(&bars->full[j % kPairStages], kPairStage);
+      const int n = max(bars->issued, bars->other_issued);
+      const uint64_t tz = globaltimer();
+      for (int j = max(n - kPairStages, 0); j < n; ++j)
+        while (!mbar_try_wait(smem_u32(&bars->full[j % kPairStages]), (j / kPairStages) & 1) &&
+               globaltimer() - tz < p.limit_ns) {
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == kWarpMma) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");

@@ -71,6 +71,12 @@ def test_product_whose_waits_run_out(T, O, L):
     _product_gives_up(T, O, L)
 
 
+@pytest.mark.parametrize("T,O,L", [(1990, 2100, 272), (300, 8200, 512), (2049, 2056, 4096)])
+def test_pairs_whose_waits_run_out(T, O, L):
+    """Pairs of CTAs: fewer stages than the ring holds, several tiles, long rows."""
+    _product_gives_up(T, O, L)
+
+
 def test_product_stall_hook_checks_its_limit():
     for bad in (0.0, -1.0, 11.0, float("nan")):
         assert _lib.load().fq_int8_debug_arm_stall(bad) == _lib.FQ_ERR_INVALID
