@@ -556,11 +556,12 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         sum.z += v[c].z * f;
         sum.w += v[c].w * f;
       }
-      const float inv = Lc > 0.0f ? 1.0f / Lc : 0.0f;
+      // (a sum of zero is a row that sees no token; one that is not a number belongs to a NaN that it sees)
+      const float inv = Lc != 0.0f ? 1.0f / Lc : 0.0f;
       const int64_t row = (s.t_first + (row0 + rr) / G) * p.q_heads + h * G + (row0 + rr) % G;
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + 4 * col) =
           make_uint2(pack16(sum.x * inv, sum.y * inv, p.fp16), pack16(sum.z * inv, sum.w * inv, p.fp16));
-      if (p.lse != nullptr && col == 0) p.lse[row] = Lc > 0.0f ? (mu + log2f(Lc)) * kLn2 : -INFINITY;
+      if (p.lse != nullptr && col == 0) p.lse[row] = Lc != 0.0f ? (mu + log2f(Lc)) * kLn2 : -INFINITY;
     }
     __syncwarp();
     cluster_sync();  // none leaves while its memory is read
@@ -568,13 +569,13 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   }
   const int64_t row = (s.t_first + (row0 + r) / G) * p.q_heads + h * G + (row0 + r) % G;
   if (whole) {
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L != 0.0f ? 1.0f / L : 0.0f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + d0);
 #pragma unroll
     for (int e = 0; e < kPer / 2; e += 2)
       *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack16(acc[2 * e] * inv, acc[2 * e + 1] * inv, p.fp16),
                                                       pack16(acc[2 * e + 2] * inv, acc[2 * e + 3] * inv, p.fp16));
-    if (p.lse != nullptr && d0 == 0) p.lse[row] = L > 0.0f ? (Mu + log2f(L)) * kLn2 : -INFINITY;
+    if (p.lse != nullptr && d0 == 0) p.lse[row] = L != 0.0f ? (Mu + log2f(L)) * kLn2 : -INFINITY;
   } else {
     float* dst = p.ws + (row * p.ws_splits + split) * (D + 4);
 #pragma unroll
@@ -678,10 +679,10 @@ kv_attn_join_kernel(const KvAttnParams p, const int few) {
       acc.w += v.w * f;
     }
   }
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const float inv = L != 0.0f ? 1.0f / L : 0.0f;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + 4 * col) =
       make_uint2(pack16(acc.x * inv, acc.y * inv, p.fp16), pack16(acc.z * inv, acc.w * inv, p.fp16));
-  if (p.lse != nullptr && col == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  if (p.lse != nullptr && col == 0) p.lse[row] = L != 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 template <int D, int NT>

@@ -668,7 +668,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const float L = l2.x + l2.y;
         const float mz = m == -INFINITY ? -INFINITY : m * c;
         const float unit = exp2i(v_top - 6);
-        const float inv = whole ? (L > 0.0f ? unit / L : 0.0f) : unit;
+        const float inv = whole ? (L != 0.0f ? unit / L : 0.0f) : unit;
         if (whole) {
           // through shared memory (this warp's rows of Q, which every MMA is done with), so that a
           // row's 16-byte pieces leave side by side
@@ -740,7 +740,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           }
         }
         if (live && whole) {
-          if (p.lse != nullptr) p.lse[row] = L > 0.0f ? (mz + log2f(L)) * kLn2 : -INFINITY;
+          if (p.lse != nullptr) p.lse[row] = L != 0.0f ? (mz + log2f(L)) * kLn2 : -INFINITY;
         } else if (live) {
           float* dst = p.ws + (row * p.ws_splits + split) * (D + 4) + D;
           dst[0] = mz;

@@ -6,12 +6,13 @@ unless a test derives its own.
 
 import time
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv import Setup
+from oracle import serving as osv
+from test_gpu_kv import HALF, Setup, f64
 from rotation_bit_quantization_token_b200 import _lib, int8_matmul
-
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,49 @@ def test_pairs_whose_waits_run_out(T, O, L):
 def test_product_stall_hook_checks_its_limit():
     for bad in (0.0, -1.0, 11.0, float("nan")):
         assert _lib.load().fq_int8_debug_arm_stall(bad) == _lib.FQ_ERR_INVALID
+
+
+# ------------------------------------------------------------------------------------
+# attention over codes that are not numbers
+# ------------------------------------------------------------------------------------
+def _with_nans(s, at):
+    """NaN codes in live tokens: (sequence, position, "k" or "v", head, element)."""
+    for b, pos, which, h, d in at:
+        (s.k if which == "k" else s.v)[s.table[b, pos // s.page], h, pos % s.page, d] = 0x7F + 0x80 * (d % 2)
+    return s
+
+
+def _check_nan_attention(s, dtype, G, causal=True, max_seq_len=None):
+    """Outputs and lse are NaN exactly where the formula's are (a row sees a NaN key; an element sees
+    a NaN value), and elsewhere within the tolerance of test_gpu_kv.py."""
+    Hq, D, n = s.H * G, s.D, s.cu[-1]
+    q = torch.randn(n, Hq, D, generator=torch.Generator().manual_seed(9)).to(dtype).cuda()
+    cache, scale, keys = s.cache(), D ** -0.5, max(s.lens)
+    out, lse = cache.attention(q, *s.batch(), max_q_len=max(s.new), max_seq_len=max_seq_len or keys, scale=scale,
+                               causal=causal, return_lse=True)
+    assert cache.device_status() == 0
+    ro, rl, info = osv.kv_attention(f64(q), s.k, s.ks, s.v, s.vs, s.cu, s.lens, s.table, scale, causal)
+    assert np.isnan(ro).any() and not np.isnan(ro).all()
+    assert np.array_equal(np.isnan(f64(lse)), np.isnan(rl))
+    assert np.array_equal(np.isnan(f64(out)), np.isnan(ro))
+    vmax = np.nanmax(np.abs(osv.E4M3)) * np.exp2(s.vs.max() - 127.0)
+    e = (D * 2.0 ** -23 + 2.0 ** -21) * np.nan_to_num(info["a"])
+    tol = ((2 * e + 2.0 ** -11 + (keys + 66) * 2.0 ** -23)[..., None] * info["pv"] + keys * 2.0 ** -25 * vmax
+           + HALF[dtype] * np.abs(ro) + 2.0 ** -25)
+    fine = ~np.isnan(ro)
+    assert np.all(np.abs(f64(out) - ro)[fine] <= tol[fine])
+    ltol = e + (keys + 64) * 2.0 ** -23 + 2.0 ** -22 * (1 + np.abs(np.nan_to_num(rl)))
+    fine = ~np.isnan(rl)
+    assert np.all(np.abs(f64(lse) - rl)[fine] <= ltol[fine])
+
+
+@pytest.mark.parametrize("new,ctx,G,longest", [
+    ([1, 1, 1], [300, 40, 700], 4, None),        # decode steps: one CTA or a cluster a sequence
+    ([1, 1, 1], [300, 40, 700], 4, 200000),      # chunks through the workspace
+    ([90, 100], [300, 256], 1, None)])           # prompts
+def test_nan_key_that_every_row_sees(new, ctx, G, longest):
+    """A NaN key among the first: the outputs of the rows that see it and their lse are NaN, not an
+    lse of a row that sees nothing."""
+    width = -(-(longest or 1) // 64)
+    s = Setup(new, ctx, H=2, D=128, page=64, seed=71, width=max(width, 16)).fill()
+    _check_nan_attention(_with_nans(s, [(0, 5, "k", 1, 3), (1, 0, "k", 0, 127)]), torch.bfloat16, G, max_seq_len=longest)
