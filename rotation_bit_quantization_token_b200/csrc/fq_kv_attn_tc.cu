@@ -28,7 +28,6 @@
 // clocks a step. TMEM: O 2 x D columns, S 2 x 128 columns (P overwrites the first half of its S).
 // Every wait is bounded. A causal prompt of 8192 tokens, 32 heads of 128 on 8: 543 us, 1.0 PFLOP/s.
 #include <cstdint>
-#include <type_traits>
 
 #include "fq_kv_common.cuh"
 
@@ -173,8 +172,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// Four codes as fp16 (the codes' values), in order: by the hardware conversion, or by moving bits
-// (finite for every pattern).
+// Four codes as fp16 (the codes' values), in order.
 __device__ __forceinline__ void cvt4(uint32_t w, uint32_t* y) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
@@ -184,12 +182,6 @@ __device__ __forceinline__ void cvt4(uint32_t w, uint32_t* y) {
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ void bits4(uint32_t w, uint32_t* y) {
-  const uint32_t k256 = 0x5C005C00u;  // codes_lo / codes_hi give code * 2^-8
-  const uint32_t lo = hmul2(codes_lo(w), k256), hi = hmul2(codes_hi(w), k256);
-  y[0] = __byte_perm(lo, hi, 0x5410);
-  y[1] = __byte_perm(lo, hi, 0x7632);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -517,43 +509,40 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const int e = 6 + bars->expo[slot][(i * 32 + key0) >> 4] - ((u & 1) ? v_top : k_top);
         f[i] = 0x00010001u * (e >= -14 ? uint32_t(e + 15) << 10 : (e >= -24 ? 1u << (e + 24) : 0u));
       }
-      auto convert = [&](auto fast) {
-#pragma unroll
-        for (int b = 0; b < kIter; b += kBatch) {
-          uint4 v[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int key = ((b + i) & 3) * 32 + key0, ch = ((b + i) >> 2) * 4 + ch0;
-            const uint32_t o = uint32_t(key * D + ch * 16);
-            v[i] = lds128(raw + (o ^ (((o >> 7) & 7u) << 4)));
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int key = ((b + i) & 3) * 32 + key0, ch = ((b + i) >> 2) * 4 + ch0;
-            const uint32_t at = dst + uint32_t((ch >> 2) * (kKeys * 128) + key * 128);
-            const uint32_t c2 = uint32_t((ch & 3) * 2), k7 = uint32_t(key & 7);
-            uint32_t y[8];
-            if constexpr (decltype(fast)::value) {
-              cvt4(v[i].x, y);
-              cvt4(v[i].y, y + 2);
-              cvt4(v[i].z, y + 4);
-              cvt4(v[i].w, y + 6);
-            } else {
-              bits4(v[i].x, y);
-              bits4(v[i].y, y + 2);
-              bits4(v[i].z, y + 4);
-              bits4(v[i].w, y + 6);
-            }
-            sts128(at + ((c2 ^ k7) << 4), hmul2(y[0], f[(b + i) & 3]), hmul2(y[1], f[(b + i) & 3]), hmul2(y[2], f[(b + i) & 3]), hmul2(y[3], f[(b + i) & 3]));
-            sts128(at + (((c2 + 1) ^ k7) << 4), hmul2(y[4], f[(b + i) & 3]), hmul2(y[5], f[(b + i) & 3]), hmul2(y[6], f[(b + i) & 3]), hmul2(y[7], f[(b + i) & 3]));
-          }
-        }
+      // address of the codes of iteration it: key (it % 4) * 32 + key0, chunk (it / 4) * 4 + ch0
+      auto codes_at = [&](int it) {
+        const uint32_t o = uint32_t(((it & 3) * 32 + key0) * D + ((it >> 2) * 4 + ch0) * 16);
+        return raw + (o ^ (((o >> 7) & 7u) << 4));
       };
-      // a step whose every key is there takes the hardware conversion (half the instructions);
-      // its codes are numbers, while stale bytes may be E4M3's NaN pattern
       const int j = u >> 1;
-      if (bars->valid[j & 15] == kAllThere && (j + 1) * kKeys <= keys) convert(std::true_type());
-      else convert(std::false_type());
+      if (bars->valid[j & 15] != kAllThere || (j + 1) * kKeys > keys) {
+        // Keys that are not there (behind the last one, on missing pages): their stale bytes may be E4M3's
+        // NaN pattern, so they are zeroed. A thread zeroes what it converts itself below.
+#pragma unroll 1
+        for (int it = 0; it < kIter; ++it) {
+          const int key = (it & 3) * 32 + key0;
+          if (j * kKeys + key >= keys || ((bars->valid[j & 15] >> (key >> 4)) & 1u) == 0u) sts128(codes_at(it), 0u, 0u, 0u, 0u);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kIter; b += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) v[i] = lds128(codes_at(b + i));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int key = ((b + i) & 3) * 32 + key0, ch = ((b + i) >> 2) * 4 + ch0;
+          const uint32_t at = dst + uint32_t((ch >> 2) * (kKeys * 128) + key * 128);
+          const uint32_t c2 = uint32_t((ch & 3) * 2), k7 = uint32_t(key & 7);
+          uint32_t y[8];
+          cvt4(v[i].x, y);
+          cvt4(v[i].y, y + 2);
+          cvt4(v[i].z, y + 4);
+          cvt4(v[i].w, y + 6);
+          sts128(at + ((c2 ^ k7) << 4), hmul2(y[0], f[(b + i) & 3]), hmul2(y[1], f[(b + i) & 3]), hmul2(y[2], f[(b + i) & 3]), hmul2(y[3], f[(b + i) & 3]));
+          sts128(at + (((c2 + 1) ^ k7) << 4), hmul2(y[4], f[(b + i) & 3]), hmul2(y[5], f[(b + i) & 3]), hmul2(y[6], f[(b + i) & 3]), hmul2(y[7], f[(b + i) & 3]));
+        }
+      }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {

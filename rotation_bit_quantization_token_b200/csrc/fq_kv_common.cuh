@@ -41,16 +41,6 @@ __device__ __forceinline__ float2 unpack16(uint32_t w, int fp16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// Codes in bytes 1 and 3 of w as two fp16 numbers (code * 2^-8): sign to bit 15, the seven
-// bits below it to bits 13 .. 7. Every bit pattern gives a finite number.
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
-  return (w & 0x80008000u) | ((w >> 1) & 0x3F803F80u);
-}
-// The same for bytes 0 and 2 (the shifts as multiplications, which run beside the logic).
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
-  return (w & 0x00800080u) * 256u + (w & 0x007F007Fu) * 128u;
-}
-
 // Exponent qe such that amax * 2^-qe lies in [2^14, 2^15) (kept where 2^-qe and 2^qe are normal).
 __device__ __forceinline__ int row_exponent(float amax) {
   const int e = int(__float_as_uint(amax) >> 23) - 127 - 14;

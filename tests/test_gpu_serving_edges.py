@@ -127,3 +127,22 @@ def test_nan_key_that_every_row_sees(new, ctx, G, longest):
     width = -(-(longest or 1) // 64)
     s = Setup(new, ctx, H=2, D=128, page=64, seed=71, width=max(width, 16)).fill()
     _check_nan_attention(_with_nans(s, [(0, 5, "k", 1, 3), (1, 0, "k", 0, 127)]), torch.bfloat16, G, max_seq_len=longest)
+
+
+@pytest.mark.parametrize("D,page,G", [(128, 64, 1), (64, 16, 4), (128, 32, 2)])
+def test_nan_keys_wherever_they_lie(D, page, G):
+    """NaN keys of cached and of new tokens, in whole steps and in the last, incomplete one of a prompt:
+    rows before them stay numbers, rows from them on are NaN."""
+    s = Setup([90, 70, 3], [300, 5, 200], H=2, D=D, page=page, seed=72).fill()
+    _check_nan_attention(_with_nans(s, [(0, 385, "k", 0, 1), (0, 388, "k", 1, 2), (1, 70, "k", 0, 9), (1, 66, "k", 1, 0),
+                                        (2, 202, "k", 0, 5), (2, 201, "k", 1, 6)]), torch.bfloat16, G)
+
+
+@pytest.mark.parametrize("D,page,G", [(128, 64, 1), (64, 16, 4), (128, 32, 2)])
+def test_nan_values_that_every_row_sees(D, page, G):
+    """NaN values of cached tokens, in whole steps and in an incomplete one (all the keys of sequence 1)."""
+    s = Setup([90, 70, 1], [300, 20, 200], H=2, D=D, page=page, seed=73).fill()
+    _check_nan_attention(_with_nans(s, [(0, 7, "v", 0, 1), (1, 3, "v", 1, 60), (1, 3, "v", 1, 61), (2, 199, "v", 0, 5)]),
+                         torch.float16, G)
+    s = Setup([90, 70], [300, 20], H=2, D=D, page=page, seed=74).fill()
+    _check_nan_attention(_with_nans(s, [(0, 389, "v", 0, 1), (1, 88, "v", 1, 60)]), torch.bfloat16, G, causal=False)
