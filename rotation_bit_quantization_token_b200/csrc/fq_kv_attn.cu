@@ -62,6 +62,8 @@ struct Geo {
 struct Shared {
   uint64_t full[kWarps][4];
   float m[kWarps][16], l[kWarps][16];
+  int nan_from[128];  // per column: see hide_nans
+  int nans;           // whether there is one
   int abort;
 };
 
@@ -182,7 +184,8 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     fence_barrier_init();
     fence_proxy_async();
   }
-  if (tid == 0) sh->abort = 0;
+  if (tid == 0) sh->abort = sh->nans = 0;
+  sh->nan_from[tid] = kNoNan;
   const int* table = p.b.page_table + int64_t(b) * p.b.table_width + (c0 >> ps_log);
   for (int i = tid; i < n_pages; i += kThreads) {
     int pg = __ldg(table + i);
@@ -277,6 +280,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     for (int e = 0; e < 2; ++e)
       if (8 * n + 2 * t4 + e < rows) all_see = min(all_see, vis[n][e]);
   all_see = __reduce_min_sync(0xffffffffu, all_see);
+  const bool uneven = all_see < keys;  // a row does not see some of the keys
   missing = __syncthreads_or(missing);  // and the scales are there
 
   float o[kS][NT][4];
@@ -327,6 +331,20 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         }
       }
       fence_proxy_async();  // the stage is written by TMA again later
+      __syncwarp();
+    }
+    if (uneven && k0 + kTK > all_see) {
+      for (int i = lane; i < kTK * (D / 16); i += 32) {
+        const int key = i / (D / 16), d = (i % (D / 16)) * 16;
+        uint4 v = lds128(vbase + swz<D>(key, d));
+        if (has_nan(v)) {
+          hide_nans(v, k0 + key, d, sh->nan_from);
+          sh->nans = 1;
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(vbase + swz<D>(key, d)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+      }
+      fence_proxy_async();
       __syncwarp();
     }
 
@@ -515,6 +533,13 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     const float* x = reinterpret_cast<const float*>(smem) + (w * kRowsTile + r) * G_::kOStride + d0;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] += x[e] * f;
+  }
+  if (sh->nans != 0) {
+    int64_t v = s.len;
+    if (p.causal) v = min(v, s.len - s.n + int64_t((row0 + r) / G) + 1);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (sh->nan_from[d0 + e] < v - c0) acc[e] = NAN;
   }
   if (meet) {
     // A CTA that gave up takes part as well (the others read its memory; the result is undefined),

@@ -62,7 +62,7 @@ struct Geo {
   static constexpr int kOffTile = 2 * kQBytes;
   static constexpr int kOffRaw = kOffTile + kTiles * kTile;
   static constexpr int kOffBars = kOffRaw + kRaws * kRaw;
-  static constexpr int kSmem = kOffBars + 1024 + 1024 /*alignment*/;
+  static constexpr int kSmem = kOffBars + 2048 + 1024 /*alignment*/;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColO = 0, kColS = 2 * D, kCols = 512;
   static_assert(kColS + 256 <= kCols, "TMEM");
@@ -84,8 +84,10 @@ struct Bars {
   // bit per 16 keys
   uint32_t valid[16];
   int8_t expo[4][8];       // per raw slot: page exponent of each 16 keys
+  int nan_from[128];       // per column: see hide_nans
+  int nans;                // whether there is one
 };
-static_assert(sizeof(Bars) <= 1024, "barrier block");
+static_assert(sizeof(Bars) <= 2048, "barrier block");
 
 // One row tile's product under one election, the whole warp running the same code: descriptors then
 // stay in uniform registers. (A leader branch with one instruction per MMA took about 110 clocks
@@ -271,6 +273,10 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     fence_barrier_init();
   }
   if (warp == kWarpMma) tmem_alloc(&bars->tmem_base, G_::kCols);
+  if (warp >= kWarpConv0) {
+    bars->nan_from[tid - kWarpConv0 * 32] = kNoNan;
+    bars->nans = 0;
+  }
   // ---- Q: kLpr lanes load a row, eight elements each; a softmax warp its own 32 rows ----
   constexpr int kLpr = D / 8, kRpi = 32 / kLpr;  // lanes per row, rows per instruction
   constexpr int kRowIter = 32 / kRpi;
@@ -492,6 +498,9 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     constexpr int kIter = kKeys * kChunks / 128;
     constexpr int kBatch = kIter < 4 ? kIter : 4;
     const int key0 = cw * 8 + (lane & 7), ch0 = lane >> 3;
+    // the first step with keys that the first row does not see
+    const int64_t all_see = p.causal ? s.len - s.n + i0 + 1 - c0 : int64_t(keys);
+    const int uneven = all_see < keys ? int(max(all_see, int64_t(0))) / kKeys : 0x7FFFFFFF;
     bool ok = true;
     for (int u = 0; ok && u < 2 * n_steps; ++u) {
       const int slot = u % G_::kRaws, tile_slot = u % G_::kTiles;
@@ -522,6 +531,20 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         for (int it = 0; it < kIter; ++it) {
           const int key = (it & 3) * 32 + key0;
           if (j * kKeys + key >= keys || ((bars->valid[j & 15] >> (key >> 4)) & 1u) == 0u) sts128(codes_at(it), 0u, 0u, 0u, 0u);
+        }
+      }
+      if ((u & 1) != 0 && j >= uneven) {
+        bool any = false;
+#pragma unroll
+        for (int it = 0; it < kIter; ++it) any = has_nan(lds128(codes_at(it))) || any;
+        if (any) {
+          bars->nans = 1;
+#pragma unroll 1
+          for (int it = 0; it < kIter; ++it) {
+            uint4 v = lds128(codes_at(it));
+            hide_nans(v, j * kKeys + (it & 3) * 32 + key0, ((it >> 2) * 4 + ch0) * 16, bars->nan_from);
+            sts128(codes_at(it), v.x, v.y, v.z, v.w);
+          }
         }
       }
 #pragma unroll
@@ -557,13 +580,13 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + G_::kColS + uint32_t(w * 128), t_o = t_lane + G_::kColO + uint32_t(w * D);
     float c = 1.0f;   // factor of a score: z log2 e = S * c
-    int64_t vis = 0;  // keys of the chunk that this thread's row sees
+    int vis = 0;      // keys of the chunk that this thread's row sees
     if (w < n_tiles) {
       const unsigned ti = (rem0 + unsigned(tr)) / Gu;
       if (p.scale != 0.0f) c = fabsf(p.scale) * kLog2e * exp2i(bars->q_exp[tr]);
       int64_t v = s.len;
       if (p.causal) v = min(v, s.len - s.n + i0 + int64_t(ti) + 1);
-      vis = tr < rows ? v - c0 : 0;
+      vis = tr < rows ? int(max(min(v - c0, int64_t(keys)), int64_t(0))) : 0;
     }
     if (p.scale != 0.0f) c = fmaxf(c * exp2i(k_top - 6), 1e-37f);  // positive: -inf * c is -inf
     float m = -INFINITY;  // the row's maximum that the exponents are taken against (of S)
@@ -574,7 +597,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         ok = warp_wait(&bars->s_full[w], j & 1, abort, p.status, kStSFull);
         if (!ok) break;
         tc_fence_after();
-        const int left = int(min(vis - int64_t(j) * kKeys, int64_t(kKeys)));  // keys of the step that the row sees
+        const int left = min(vis - j * kKeys, kKeys);  // keys of the step that the row sees
         const uint32_t valid = bars->valid[j & 15];
         const bool masked = __any_sync(0xffffffffu, left < kKeys) || valid != kAllThere;
         float x[kKeys];
@@ -658,6 +681,12 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const float mz = m == -INFINITY ? -INFINITY : m * c;
         const float unit = exp2i(v_top - 6);
         const float inv = whole ? (L != 0.0f ? unit / L : 0.0f) : unit;
+        const bool nans = bars->nans != 0;
+        auto show_nans = [&](uint32_t* o, int col) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (bars->nan_from[col + e] < vis) o[e] = 0x7FFFFFFFu;
+        };
         if (whole) {
           // through shared memory (this warp's rows of Q, which every MMA is done with), so that a
           // row's 16-byte pieces leave side by side
@@ -673,6 +702,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = 0u;
             }
+            if (nans) show_nans(o, i);
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               uint32_t y[4];
@@ -709,6 +739,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             uint32_t o[32];
             tmem_ld32(t_o + uint32_t(i), o);
             tmem_wait_ld();
+            if (nans) show_nans(o, i);
             __syncwarp();  // the last columns have been read
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {

@@ -79,6 +79,28 @@ __device__ __forceinline__ Rows sequence_rows(const KvAttnParams& p, int b, int6
   return r;
 }
 
+// A product with a probability of zero keeps a NaN of V, so in a tile of keys that some of the rows do
+// not see, V's NaN codes are replaced by zeros, and the first key (of the chunk) that has one in column d
+// is kept in nan_from[d]. What a row sees are the keys up to some one, so its output is NaN in the
+// columns whose nan_from lies among them.
+constexpr int kNoNan = 0x7FFFFFFF;
+// Whether one of 16 codes is NaN: 1 added to its low seven bits carries into the eighth.
+__device__ __forceinline__ bool has_nan(const uint4& v) {
+  auto carry = [](uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; };
+  return ((carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80808080u) != 0u;
+}
+// Replaces the NaNs among 16 codes of one key, columns d0 .. d0 + 15.
+__device__ __forceinline__ void hide_nans(uint4& v, int key, int d0, int* nan_from) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t nan = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    w[i] &= ~nan;
+    for (int e = 0; e < 4; ++e)
+      if ((nan >> (8 * e)) & 1u) atomicMin(nan_from + d0 + 4 * i + e, key);
+  }
+}
+
 // Whether the tensor-core kernel takes a sequence with n new tokens (else the other one does):
 // more than p.tc_rows rows. Both kernels and the join decide by it.
 __device__ __forceinline__ bool takes_tc(const KvAttnParams& p, int64_t n, int G) { return n * G > p.tc_rows; }

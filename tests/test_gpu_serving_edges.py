@@ -146,3 +146,21 @@ def test_nan_values_that_every_row_sees(D, page, G):
                          torch.float16, G)
     s = Setup([90, 70], [300, 20], H=2, D=D, page=page, seed=74).fill()
     _check_nan_attention(_with_nans(s, [(0, 389, "v", 0, 1), (1, 88, "v", 1, 60)]), torch.bfloat16, G, causal=False)
+
+
+@pytest.mark.parametrize("new,ctx,G,longest", [
+    ([3, 2, 1], [100, 700, 30], 4, None),        # a few new tokens each
+    ([4, 2, 1], [100, 700, 30], 4, 200000),      # in chunks
+    ([90, 300, 65], [300, 5, 0], 1, None),       # prompts
+    ([120], [3000], 2, None)])                   # a prompt in chunks
+@pytest.mark.parametrize("D,page", [(128, 64), (64, 16)])
+def test_nan_values_behind_a_row(new, ctx, G, longest, D, page):
+    """NaN values of the new tokens themselves: they reach the rows that see them, in their elements
+    only, and no row before them."""
+    s = Setup(new, ctx, H=2, D=D, page=page, seed=75, width=-(-(longest or 4000) // page)).fill()
+    at = []
+    for b, n in enumerate(s.new):
+        for back, h, d in ((1, 0, 0), (2, 1, 7), (n // 2 + 1, 0, D - 1), (n // 2 + 1, 0, 0), (n - 1, 1, 33)):
+            if 0 < back <= n:
+                at.append((b, s.lens[b] - back, "v", h, d))
+    _check_nan_attention(_with_nans(s, at), torch.bfloat16, G, max_seq_len=longest)
