@@ -278,10 +278,10 @@ FQ_API fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch
  *               two streams, or two captured graphs) need one each
  * Sums, maxima and the softmax are float32. Keys and values enter the products exactly (an E4M3
  * code is an fp16 number), queries too, scaled by a power of two per row, but for elements 2^-29
- * below the row's largest; the probabilities are rounded to fp16 for the second product. Sequences
- * of more than 64 (token, query head) pairs per key / value head are computed in units of the
- * largest page scale among up to some thousands of their tokens: codes of pages 2^-21 of it or
- * less lose low bits there. Scores past the float32 range and NaN in q are outside the contract.
+ * below the row's largest; the probabilities are rounded to fp16 for the second product. The scales
+ * of the pages may lie as far apart as their range allows. A NaN code makes the outputs NaN of the
+ * rows that see its token: a key's whole rows and their lse, a value's element. Scores past the
+ * float32 range and NaN in q are outside the contract.
  * Stale rows of a page (behind the last token) are never
  * used, whatever they hold. Allocates nothing; asynchronous on stream; deterministic. Errors:
  * FQ_ERR_NULLPTR, FQ_ERR_INVALID (also a workspace that is too small), FQ_ERR_CUDA. */

@@ -4,16 +4,21 @@
 // A row is a (new token, query head of the group) pair; one CTA takes two tiles of 128 rows of
 // one sequence and key / value head, and a chunk of keys, 128 keys at a time:
 //     S = Q K^T   (M = 128 rows, N = 128 keys, K = D; Q and K fp16 in shared memory)
-//     P = exp2(S c - m c)                      (registers, one thread per row)
+//     P = exp2(S c - m)                        (registers, one thread per row)
 //     O += P V    (M = 128 rows, N = D, K = 128 keys; P fp16 in TMEM, V fp16 in shared memory)
 // The two row tiles take turns: while one's softmax runs, the tensor cores do the other's products.
 // Both share every converted tile of K and V.
 //
 // Codes reach the MMAs as fp16, converted by a warpgroup that also multiplies by the page's power of
-// two relative to the largest exponent among the chunk's pages, times 2^6: codes of pages down to
-// 2^-21 of the largest keep all their bits. One power of two per row and one per output then undo
-// all scaling: the score's factor c holds the softmax scale, log2 e, the q row's exponent and the
-// keys' largest page exponent.
+// two in the step's units, exactly: code * 2^e is an fp16 number for e in [-15, 7]. Where all pages of
+// the CTA's keys lie within 2^15 of one another (their values; their keys), the largest one's are the
+// units of every step. Else each step has its own: keys in units of its largest page, undone by the
+// factor c of its scores (beside the softmax scale, log2 e and the q row's exponent); values in units
+// that last as long as pages stay within [-15, 0] of it, and when they change, O is multiplied by the
+// power of two between them. Pages of one step that lie further apart are taken in steps of their own,
+// each over the same 128 keys with the other pages left out. (The producer is short of issue slots
+// beside the softmax: with the units of every step worked out in every CTA the 8192-token prompt took
+// 607 us, now 551.)
 //
 // Softmax. A thread owns one row (its TMEM lane), so no exchange is needed. The maximum that the
 // exponents are taken against is only raised when a row exceeds it by 2^15 (the probabilities then
@@ -26,7 +31,7 @@
 // warps (about 200 clocks each), and a step of one row tile is a chain of softmax (2000 clocks), its
 // hand-over, P V and S (1024), and their hand-over back; the two row tiles' chains overlap, about 3800
 // clocks a step. TMEM: O 2 x D columns, S 2 x 128 columns (P overwrites the first half of its S).
-// Every wait is bounded. A causal prompt of 8192 tokens, 32 heads of 128 on 8: 543 us, 1.0 PFLOP/s.
+// Every wait is bounded. A causal prompt of 8192 tokens, 32 heads of 128 on 8: 551 us, 1.0 PFLOP/s.
 #include <cstdint>
 
 #include "fq_kv_common.cuh"
@@ -42,7 +47,8 @@ constexpr int kKeys = 128;  // keys of a step
 constexpr int kSorted = 256;  // sequences that are taken in order of length
 constexpr int kWarpMma = 0, kWarpProducer = 1, kWarpSoft0 = 4, kWarpConv0 = 12;
 // Register split (setmaxnreg): launched at 128 per thread; 2 softmax warpgroups, the converters, the rest
-constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsConv = 72, kRegsLow = 40;
+// (200, 72 and 40: 559 us for 551)
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 192, kRegsConv = 72, kRegsLow = 56;
 static_assert(128 * (2 * kRegsSoftmax + kRegsConv + kRegsLow) <= kThreads * kRegsLaunch, "register split");
 
 enum : uint32_t {
@@ -51,6 +57,8 @@ enum : uint32_t {
 };
 
 constexpr uint32_t kAllThere = (1u << (kKeys / 16)) - 1u;  // a step with all its pages
+constexpr uint32_t kChange = 1u << 31, kLast = 1u << 30;
+constexpr int kNoPage = -1000;  // no exponent
 
 template <int D>
 struct Geo {
@@ -68,6 +76,13 @@ struct Geo {
   static_assert(kColS + 256 <= kCols, "TMEM");
 };
 
+// What the producer tells about a step that differs from the one before in more than its pages.
+struct __align__(16) Step {
+  int first;       // first key (of the chunk); else 128 further on
+  float k_factor;  // 2^(exponent of the keys' unit - 6)
+  int v_unit;      // exponent of the values' unit
+};
+
 struct Bars {
   // unit u = 2j is K of step j, u = 2j + 1 V of step j
   uint64_t raw_full[4], raw_empty[4];  // codes of unit u, slot u % 4
@@ -77,13 +92,14 @@ struct Bars {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
-  int k_top[8], v_top[8];            // largest page exponents of the CTA's keys, by scanning warp
+  int4 range[8];                     // largest exponent and least (negated) of the pages' keys, and of their values, by scanning warp
   int8_t q_exp[kTcRows];   // exponents of Q's rows
   int sorted;
-  // per step (mod 16; the producer is at most 4 + 3 steps ahead): the step's pages that are there, one
-  // bit per 16 keys
+  // per step (mod 16; the producer is at most 4 + 3 steps ahead): the pages that are there, one bit per 16
+  // keys, kChange where the step's other properties are to be read, kLast in the last step
   uint32_t valid[16];
-  int8_t expo[4][8];       // per raw slot: page exponent of each 16 keys
+  Step step[16];
+  int8_t expo[4][8];       // per raw slot: exponent of each 16 keys in the step's units
   int nan_from[128];       // per column: see hide_nans
   int nans;                // whether there is one
 };
@@ -185,6 +201,42 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// The scale bytes (as page_exp allows them) of the pages of a step's eight times 16 keys.
+struct Pages {
+  uint32_t k[2], v[2];
+};
+constexpr int kSpan = 15;  // exponents of a step's pages differ by this at most
+__device__ __forceinline__ uint32_t bytes_of(uint32_t bits) {  // 0xFF for each of four bits
+  return ((bits * 0x00204081u) & 0x01010101u) * 0xFFu;
+}
+__device__ __forceinline__ uint32_t top_byte(const uint32_t* w, uint32_t mask) {
+  uint32_t x = __vmaxu4(w[0] & bytes_of(mask & 15u), w[1] & bytes_of(mask >> 4));
+  x = __vmaxu4(x, x >> 16);
+  return __vmaxu4(x, x >> 8) & 0xFFu;
+}
+__device__ __forceinline__ uint32_t least_byte(const uint32_t* w, uint32_t mask) {
+  uint32_t x = __vminu4(w[0] | ~bytes_of(mask & 15u), w[1] | ~bytes_of(mask >> 4));
+  x = __vminu4(x, x >> 16);
+  return __vminu4(x, x >> 8) & 0xFFu;
+}
+// Which of the pages `left` (a bit each, not empty) a step takes: all of them where they lie within
+// kSpan of one another, else the first and those within kSpan / 2 of it.
+__device__ __forceinline__ uint32_t next_pages(const Pages& g, uint32_t left) {
+  if (int(top_byte(g.k, left) - least_byte(g.k, left)) <= kSpan && int(top_byte(g.v, left) - least_byte(g.v, left)) <= kSpan)
+    return left;
+  const uint32_t first = left & (0u - left);
+  const uint32_t k0 = top_byte(g.k, first) * 0x01010101u, v0 = top_byte(g.v, first) * 0x01010101u;
+  uint32_t take = 0u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    constexpr uint32_t kNear = uint32_t(kSpan / 2) * 0x01010101u;
+    uint32_t near = __vcmpleu4(__vabsdiffu4(g.k[i], k0), kNear) & __vcmpleu4(__vabsdiffu4(g.v[i], v0), kNear) & 0x08040201u;
+    near |= near >> 16;
+    near |= near >> 8;
+    take |= (near & 15u) << (4 * i);
+  }
+  return take & left;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -244,7 +296,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const int64_t i0 = quotient(row0, G);
   const unsigned rem0 = unsigned(row0 - i0 * G), Gu = unsigned(G);
   const int64_t tok0 = s.t_first + i0;
-  const int n_steps = (keys + kKeys - 1) / kKeys;
+  const int n_windows = (keys + kKeys - 1) / kKeys;  // of 128 keys
   const int n_tiles = rows > 128 ? 2 : 1;  // row tiles with rows
   const int ps_log = 31 - __clz(ps);
   const int* table = p.b.page_table + int64_t(b) * p.b.table_width + (c0 >> ps_log);
@@ -252,8 +304,8 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
   // The beginning of a CTA, by parts that run at the same time (11000 clocks to the first softmax, 13000
   // one after the other; an average CTA of an 8192-token prompt takes 140000): the producer sets up the
-  // mbarriers and starts loading, warp 0 allocates TMEM, the softmax warps bring Q, the others look for
-  // the largest page exponents.
+  // mbarriers and starts loading, warp 0 allocates TMEM, the softmax warps bring Q, the others count the
+  // steps.
   if (warp == kWarpProducer && lane == 0) {
     for (int i = 0; i < G_::kRaws; ++i) {
       mbar_init(&bars->raw_full[i], 1);
@@ -326,11 +378,12 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     fence_proxy_async();
   }
 
-  // ---- the largest page exponents, four pages of a thread at a time ----
+  // ---- the range of the page exponents, four pages of a thread at a time ----
   constexpr int kScanWarps = kWarps - 9;  // all but the producer and the softmax
-  const int scan = warp < kWarpProducer ? warp : (warp < kWarpSoft0 ? warp - 1 : (warp >= kWarpConv0 ? warp - 9 : -1));
+  static_assert(kWarpMma == 0 && kWarpProducer == 1 && kWarpSoft0 == 4 && kWarpConv0 == 12, "warps 0, 2, 3 and 12-15 scan");
+  const int scan = warp == 0 ? 0 : (warp == 2 || warp == 3 ? warp - 1 : (warp >= kWarpConv0 ? warp - 9 : -1));
   if (scan >= 0) {
-    int kt = kPageExpMin, vt = kPageExpMin;
+    int kt = kNoPage, kl = -kNoPage, vt = kNoPage, vl = -kNoPage;  // largest and least of keys and values
     for (int i = scan * 32 + lane; i < n_pages; i += 4 * 32 * kScanWarps) {
       int pg[4];
 #pragma unroll
@@ -340,38 +393,39 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const bool there = pg[e] >= 0 && int64_t(pg[e]) < p.c.num_pages;
         const int64_t at = int64_t(there ? pg[e] : 0) * H + h;
         const int ke = page_exp(__ldg(p.c.k_scale + at)), ve = page_exp(__ldg(p.c.v_scale + at));
-        kt = max(kt, there ? ke : kPageExpMin);
-        vt = max(vt, there ? ve : kPageExpMin);
-        if (!there && p.status != nullptr) atomicOr(p.status, FQ_KV_BAD_BATCH);
+        if (there) {
+          kt = max(kt, ke);
+          kl = min(kl, ke);
+          vt = max(vt, ve);
+          vl = min(vl, ve);
+        } else if (p.status != nullptr) {
+          atomicOr(p.status, FQ_KV_BAD_BATCH);
+        }
       }
     }
     kt = __reduce_max_sync(0xffffffffu, kt);
+    kl = __reduce_min_sync(0xffffffffu, kl);
     vt = __reduce_max_sync(0xffffffffu, vt);
-    if (lane == 0) {
-      bars->k_top[scan] = kt;
-      bars->v_top[scan] = vt;
-    }
+    vl = __reduce_min_sync(0xffffffffu, vl);
+    if (lane == 0) bars->range[scan] = make_int4(kt, -kl, vt, -vl);
   }
-  // Barrier 1: the exponents and mbarriers are there (the converters wait for no more); barrier 2:
-  // Q and TMEM too. The producer waits for neither.
+  // Barrier 1: the range and mbarriers are there (the converters and the producer, which has
+  // asked for the first 128 keys' codes by then, wait for no more); barrier 2: Q and TMEM too.
   constexpr int kMeetScan = 1, kMeetAll = 2;
   uint32_t tmem = 0;
-  int k_top = 0, v_top = 0;
   tc_fence_before();
   __syncwarp();
   if (warp >= kWarpConv0) {
     named_bar(kMeetScan, 32 * (kScanWarps + 1));
     named_bar_arrive(kMeetAll, kThreads);
   } else {
-    if (scan >= 0 || warp == kWarpProducer) named_bar_arrive(kMeetScan, 32 * (kScanWarps + 1));
+    if (scan >= 0) named_bar_arrive(kMeetScan, 32 * (kScanWarps + 1));
     if (warp == kWarpMma || warp >= kWarpSoft0) named_bar(kMeetAll, kThreads);
     else named_bar_arrive(kMeetAll, kThreads);
   }
   tc_fence_after();
   if (warp == kWarpMma || warp >= kWarpSoft0) {
     tmem = bars->tmem_base;
-    k_top = __reduce_max_sync(0xffffffffu, bars->k_top[min(lane, kScanWarps - 1)]);
-    v_top = __reduce_max_sync(0xffffffffu, bars->v_top[min(lane, kScanWarps - 1)]);
   }
   int* abort = &bars->abort;
 
@@ -382,45 +436,121 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     // whose keys begin a TMA box issues the box.
     setmaxnreg_dec<kRegsLow>();
     const int box = ps < kKeys ? ps : kKeys;
-    auto page_of = [&](int j) {  // page of this lane's keys in step j, -1: none
-      const int key = j * kKeys + lane * 16;
-      if (lane >= kKeys / 16 || j >= n_steps || key >= keys) return -1;
+    auto page_of = [&](int w) {  // page of this lane's keys among 128, -1: none
+      const int key = w * kKeys + lane * 16;
+      if (lane >= kKeys / 16 || w >= n_windows || key >= keys) return -1;
       const int pg = __ldg(table + (key >> ps_log));
       return pg >= 0 && int64_t(pg) < p.c.num_pages ? pg : -1;
     };
-    auto bytes_of = [&](int pg) {
+    auto bytes_of_page = [&](int pg) {
       if (pg < 0) return 0u;
       return uint32_t(__ldg(p.c.k_scale + int64_t(pg) * H + h)) | (uint32_t(__ldg(p.c.v_scale + int64_t(pg) * H + h)) << 8);
     };
     int pg0 = page_of(0), pg1 = page_of(1);
-    uint32_t by0 = bytes_of(pg0);
-    bool ok = true;
-    int issued = 0;  // units
-    for (int j = 0; ok && j < n_steps; ++j) {
-      const int pg2 = page_of(j + 2);
-      const uint32_t by1 = bytes_of(pg1);
-      const bool first_of_box = lane < kKeys / 16 && (lane * 16) % box == 0 && pg0 >= 0;
-      const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, first_of_box));
-      const uint32_t valid = __ballot_sync(0xffffffffu, pg0 >= 0);
-      const int row = int(((int64_t(max(pg0, 0)) * H + h) * ps + ((j * kKeys + lane * 16) & (ps - 1))) * D / 128);
+    auto row_of = [&](int pg, int w) {  // of the tensor maps
+      return int(((int64_t(max(pg, 0)) * H + h) * ps + ((w * kKeys + lane * 16) & (ps - 1))) * D / 128);
+    };
+    auto ask = [&](int kv, int row, int slot) {
+      tma_load_2d(sbase + uint32_t(G_::kOffRaw + slot * G_::kRaw + lane * 16 * D), kv == 0 ? &map_k : &map_v, 0, row,
+                  &bars->raw_full[slot]);
+    };
+    const bool box_begins = lane < kKeys / 16 && (lane * 16) % box == 0;
+    // the first two steps are asked for at once (where such a step takes only some of the pages, the
+    // others' codes are zeroed)
+    const int n_early = min(n_windows, 2);
+    for (int w = 0; w < n_early; ++w) {
+      const bool begins = box_begins && (w == 0 ? pg0 : pg1) >= 0;
+      const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, begins));
 #pragma unroll
-      for (int w = 0; ok && w < 2; ++w) {
-        const int u = 2 * j + w, slot = u % G_::kRaws;
+      for (int kv = 0; kv < 2; ++kv) {
+        if (lane == 0) mbar_expect_tx(&bars->raw_full[2 * w + kv], boxes * uint32_t(box * D));
+        __syncwarp();
+        if (begins) ask(kv, row_of(w == 0 ? pg0 : pg1, w), 2 * w + kv);
+      }
+    }
+    uint32_t by0 = bytes_of_page(pg0);
+    named_bar(kMeetScan, 32 * (kScanWarps + 1));
+    const int4 r = bars->range[min(lane, kScanWarps - 1)];
+    const int kt = __reduce_max_sync(0xffffffffu, r.x), kl = -__reduce_max_sync(0xffffffffu, r.y);
+    const int vt = __reduce_max_sync(0xffffffffu, r.z), vl = -__reduce_max_sync(0xffffffffu, r.w);
+    const bool apart = kt - kl > kSpan || vt - vl > kSpan;
+    bool ok = true;
+    int issued = 2 * n_early;  // units
+    int j = 0;                 // step
+    int k_unit = max(kt, kPageExpMin), v_unit = max(vt, kPageExpMin);  // exponents of the keys' and values' units
+    // Step j: the pages `take` of keys w * 128 .. , this lane's with tensor map row `row` and exponents ke, ve.
+    auto step = [&](uint32_t take, int w, int row, int ke, int ve, bool change, bool last) {
+      const bool in = ((take >> lane) & 1u) != 0u;
+#pragma unroll
+      for (int kv = 0; ok && kv < 2; ++kv) {
+        const int u = 2 * j + kv, slot = u % G_::kRaws;
         ok = u < G_::kRaws || warp_wait(&bars->raw_empty[slot], (u / G_::kRaws - 1) & 1, abort, p.status, kStRawEmpty);
         if (!ok) break;
-        if (lane < kKeys / 16) bars->expo[slot][lane] = int8_t(page_exp(w == 0 ? by0 & 0xFFu : by0 >> 8));
-        if (w == 0 && lane == 0) bars->valid[j & 15] = valid;
+        if (lane < kKeys / 16) bars->expo[slot][lane] = int8_t(!in ? 0 : (kv == 0 ? ke - k_unit + 6 : ve - v_unit));
+        if (kv == 0 && lane == 0) {
+          bars->valid[j & 15] = take | (change ? kChange : 0u) | (last ? kLast : 0u);
+          if (change) bars->step[j & 15] = Step{w * kKeys, exp2i(k_unit - 6), v_unit};
+        }
         __syncwarp();
+        if (j < n_early) {  // asked for above
+          if (lane == 0) mbar_arrive(&bars->raw_full[slot]);
+          continue;
+        }
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, in && box_begins));
         if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[slot], boxes * uint32_t(box * D));
         __syncwarp();
-        if (first_of_box)
-          tma_load_2d(sbase + uint32_t(G_::kOffRaw + slot * G_::kRaw + lane * 16 * D), w == 0 ? &map_k : &map_v, 0, row,
-                      &bars->raw_full[slot]);
+        if (in && box_begins) ask(kv, row, slot);
         issued = u + 1;
       }
-      pg0 = pg1;
-      pg1 = pg2;
-      by0 = by1;
+      ++j;
+    };
+    if (!apart) {
+      for (int w = 0; ok && w < n_windows; ++w) {
+        const int pg2 = page_of(w + 2);
+        const uint32_t by1 = bytes_of_page(pg1);
+        step(__ballot_sync(0xffffffffu, pg0 >= 0), w, row_of(pg0, w), page_exp(by0 & 0xFFu), page_exp(by0 >> 8), w == 0,
+             w + 1 == n_windows);
+        pg0 = pg1;
+        pg1 = pg2;
+        by0 = by1;
+      }
+    } else {
+      // first a step for each 128 keys, then those of the pages that were left out
+      bool have_unit = false;
+      int behind = 0;  // times 128 keys with such pages
+#pragma unroll 1
+      for (int pass = 0; pass < 2 && (pass == 0 || behind > 0); ++pass) {
+#pragma unroll 1
+        for (int w = 0; ok && w < n_windows; ++w) {
+          pg0 = page_of(w);
+          by0 = bytes_of_page(pg0);
+          const int ke = page_exp(by0 & 0xFFu), ve = page_exp(by0 >> 8);
+          Pages g;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const bool mine = (lane >> 2) == i;
+            g.k[i] = __reduce_or_sync(0xffffffffu, mine ? uint32_t(ke + 127) << (8 * (lane & 3)) : 0u);
+            g.v[i] = __reduce_or_sync(0xffffffffu, mine ? uint32_t(ve + 127) << (8 * (lane & 3)) : 0u);
+          }
+          uint32_t left = __ballot_sync(0xffffffffu, pg0 >= 0);
+          uint32_t take = left != 0u ? next_pages(g, left) : 0u;
+          if (left != take) behind += pass == 0 ? 1 : -1;
+          if (pass == 1) left &= ~take;
+          while (ok && (pass == 0 || left != 0u)) {
+            if (pass == 1) take = next_pages(g, left);
+            if (take != 0u) {
+              k_unit = int(top_byte(g.k, take)) - 127;
+              const int hi = int(top_byte(g.v, take)) - 127, lo = int(least_byte(g.v, take)) - 127;
+              // a new unit leaves room above and below, so that neighbouring pages seldom need another
+              if (!have_unit || hi > v_unit || lo < v_unit - kSpan) v_unit = hi + min(kSpan / 3, kSpan - (hi - lo));
+              have_unit = true;
+            }
+            left &= ~take;
+            step(take, w, row_of(pg0, w), ke, ve, true, behind == 0 && (pass == 0 ? w + 1 == n_windows : left == 0u));
+            if (pass == 0) break;
+          }
+        }
+      }
     }
     // the last copies have landed before the CTA may exit (the converters wait for each of them;
     // after an abort they may have left)
@@ -451,17 +581,20 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       commit_e(&bars->s_full[w]);
       if (w == n_tiles - 1) commit_e(&bars->t_empty[slot]);
     };
-    bool ok = n_steps > 0 && wait_tile(0, kStKFull);
+    bool ok = wait_tile(0, kStKFull);
     if (ok) {
       tc_fence_after();
       for (int w = 0; w < n_tiles; ++w) scores(w, 0);
     }
     // P V of step j, then the row tile's next scores, which overwrite P
-    for (int j = 0; ok && j < n_steps; ++j) {
+    bool last = !ok || (bars->valid[0] & kLast) != 0u;
+    for (int j = 0, end = 0; ok && !end; ++j) {
       const int slot = (2 * j + 1) % G_::kTiles;
       const uint64_t v = desc_lbo(sbase + uint32_t(G_::kOffTile + slot * G_::kTile), kKeys * 128);
       // K of the next step, whose conversion follows V's of this one (or V alone in the last step)
-      ok = wait_tile(j + 1 < n_steps ? 2 * j + 2 : 2 * j + 1, j + 1 < n_steps ? kStKFull : kStVFull);
+      ok = wait_tile(last ? 2 * j + 1 : 2 * j + 2, last ? kStVFull : kStKFull);
+      end = last;
+      const uint32_t next = last ? 0u : bars->valid[(j + 1) & 15];
       for (int w = 0; ok && w < n_tiles; ++w) {
         const uint32_t t_o = tmem + G_::kColO + uint32_t(w * D), t_p = tmem + G_::kColS + uint32_t(w * 128);
         ok = warp_wait(&bars->p_full[w], j & 1, abort, p.status, kStPFull);
@@ -469,12 +602,13 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         tc_fence_after();
         mma_values<8>(t_o, t_p, v, kIdO, j > 0 ? 1u : 0u);
         if (w == n_tiles - 1) commit_e(&bars->t_empty[slot]);
-        if (j + 1 < n_steps) {
+        if (!last) {
           scores(w, j + 1);
         } else {
           commit_e(&bars->o_full[w]);
         }
       }
+      last = (next & kLast) != 0u;
     }
     // every MMA issued here has completed before TMEM is released
     commit_e(&bars->mma_done);
@@ -498,11 +632,13 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     constexpr int kIter = kKeys * kChunks / 128;
     constexpr int kBatch = kIter < 4 ? kIter : 4;
     const int key0 = cw * 8 + (lane & 7), ch0 = lane >> 3;
-    // the first step with keys that the first row does not see
+    // the first 128 keys with some that the first row does not see
     const int64_t all_see = p.causal ? s.len - s.n + i0 + 1 - c0 : int64_t(keys);
-    const int uneven = all_see < keys ? int(max(all_see, int64_t(0))) / kKeys : 0x7FFFFFFF;
+    const int uneven = all_see < keys ? int(max(all_see, int64_t(0))) / kKeys * kKeys : 0x7FFFFFFF;
     bool ok = true;
-    for (int u = 0; ok && u < 2 * n_steps; ++u) {
+    int first = 0;  // first key of the step
+    int u = 0;
+    for (bool end = false; ok && !end; ++u) {
       const int slot = u % G_::kRaws, tile_slot = u % G_::kTiles;
       ok = warp_wait(&bars->raw_full[slot], (u / G_::kRaws) & 1, abort, p.status, kStRawFull);
       if (ok && u >= G_::kTiles)
@@ -511,29 +647,33 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       const uint32_t raw = sbase + uint32_t(G_::kOffRaw + slot * G_::kRaw);
       const uint32_t dst = sbase + uint32_t(G_::kOffTile + tile_slot * G_::kTile);
       // iteration it of a warp: eight keys (it % 4) * 32 + key0, chunks (it / 4) * 4 + ch0. A key's
-      // factor: 2^(6 + exponent - top), zero below the range of fp16
+      // factor: 2^expo, expo in [-15, 6]
       uint32_t f[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int e = 6 + bars->expo[slot][(i * 32 + key0) >> 4] - ((u & 1) ? v_top : k_top);
-        f[i] = 0x00010001u * (e >= -14 ? uint32_t(e + 15) << 10 : (e >= -24 ? 1u << (e + 24) : 0u));
+        const int e = bars->expo[slot][(i * 32 + key0) >> 4];
+        f[i] = 0x00010001u * (e >= -14 ? uint32_t(e + 15) << 10 : 1u << 9);
       }
       // address of the codes of iteration it: key (it % 4) * 32 + key0, chunk (it / 4) * 4 + ch0
       auto codes_at = [&](int it) {
         const uint32_t o = uint32_t(((it & 3) * 32 + key0) * D + ((it >> 2) * 4 + ch0) * 16);
         return raw + (o ^ (((o >> 7) & 7u) << 4));
       };
-      const int j = u >> 1;
-      if (bars->valid[j & 15] != kAllThere || (j + 1) * kKeys > keys) {
-        // Keys that are not there (behind the last one, on missing pages): their stale bytes may be E4M3's
-        // NaN pattern, so they are zeroed. A thread zeroes what it converts itself below.
+      uint32_t valid = bars->valid[(u >> 1) & 15];
+      if ((u & 1) == 0) first += kKeys;
+      else end = (valid & kLast) != 0u;
+      if ((valid & kChange) != 0u) first = bars->step[(u >> 1) & 15].first;
+      valid &= kAllThere;
+      if (valid != kAllThere || first + kKeys > keys) {
+        // Keys that are not there (behind the last one, on missing pages or those of another step): their stale
+        // bytes may be E4M3's NaN pattern, so they are zeroed. A thread zeroes what it converts itself below.
 #pragma unroll 1
         for (int it = 0; it < kIter; ++it) {
           const int key = (it & 3) * 32 + key0;
-          if (j * kKeys + key >= keys || ((bars->valid[j & 15] >> (key >> 4)) & 1u) == 0u) sts128(codes_at(it), 0u, 0u, 0u, 0u);
+          if (first + key >= keys || ((valid >> (key >> 4)) & 1u) == 0u) sts128(codes_at(it), 0u, 0u, 0u, 0u);
         }
       }
-      if ((u & 1) != 0 && j >= uneven) {
+      if ((u & 1) != 0 && first >= uneven) {
         bool any = false;
 #pragma unroll
         for (int it = 0; it < kIter; ++it) any = has_nan(lds128(codes_at(it))) || any;
@@ -542,7 +682,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll 1
           for (int it = 0; it < kIter; ++it) {
             uint4 v = lds128(codes_at(it));
-            hide_nans(v, j * kKeys + (it & 3) * 32 + key0, ((it >> 2) * 4 + ch0) * 16, bars->nan_from);
+            hide_nans(v, first + (it & 3) * 32 + key0, ((it >> 2) * 4 + ch0) * 16, bars->nan_from);
             sts128(codes_at(it), v.x, v.y, v.z, v.w);
           }
         }
@@ -579,26 +719,38 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const int w = (warp - kWarpSoft0) >> 2, tr = tid - kWarpSoft0 * 32;  // row of the CTA
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + G_::kColS + uint32_t(w * 128), t_o = t_lane + G_::kColO + uint32_t(w * D);
-    float c = 1.0f;   // factor of a score: z log2 e = S * c
+    float c_row = 1.0f;  // factor of the row's scores, but for the keys' unit
+    float c = 1.0f;      // with it: z log2 e = S * c
     int vis = 0;      // keys of the chunk that this thread's row sees
     if (w < n_tiles) {
       const unsigned ti = (rem0 + unsigned(tr)) / Gu;
-      if (p.scale != 0.0f) c = fabsf(p.scale) * kLog2e * exp2i(bars->q_exp[tr]);
+      if (p.scale != 0.0f) c_row = fabsf(p.scale) * kLog2e * exp2i(bars->q_exp[tr]);
       int64_t v = s.len;
       if (p.causal) v = min(v, s.len - s.n + i0 + int64_t(ti) + 1);
       vis = tr < rows ? int(max(min(v - c0, int64_t(keys)), int64_t(0))) : 0;
     }
-    if (p.scale != 0.0f) c = fmaxf(c * exp2i(k_top - 6), 1e-37f);  // positive: -inf * c is -inf
-    float m = -INFINITY;  // the row's maximum that the exponents are taken against (of S)
+    float m = -INFINITY;  // the row's maximum that the exponents are taken against (of z log2 e = S * c)
+    int unit = 0;         // of O
+    int ahead = 0;        // vis, less what the step's first key is beyond j * kKeys
     float2 l2 = make_float2(0.0f, 0.0f);
     bool ok = true;
     if (w < n_tiles) {
-      for (int j = 0; j < n_steps; ++j) {
+      bool end = false;
+      for (int j = 0; !end; ++j) {
         ok = warp_wait(&bars->s_full[w], j & 1, abort, p.status, kStSFull);
         if (!ok) break;
         tc_fence_after();
-        const int left = min(vis - j * kKeys, kKeys);  // keys of the step that the row sees
-        const uint32_t valid = bars->valid[j & 15];
+        uint32_t valid = bars->valid[j & 15];
+        int to = unit;
+        end = (valid & kLast) != 0u;
+        if ((valid & kChange) != 0u) {
+          const Step st = bars->step[j & 15];
+          ahead = vis - (st.first - j * kKeys);
+          c = fmaxf(c_row * st.k_factor, 1e-37f);  // positive: -inf * c is -inf
+          to = st.v_unit;
+        }
+        valid &= kAllThere;
+        const int left = min(ahead - j * kKeys, kKeys);  // keys of the step that the row sees
         const bool masked = __any_sync(0xffffffffu, left < kKeys) || valid != kAllThere;
         float x[kKeys];
         auto load = [&]() {
@@ -622,14 +774,16 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         }
         a0 = max3(a0, x[kKeys - 4], x[kKeys - 3]);
         a1 = max3(a1, x[kKeys - 2], x[kKeys - 1]);
-        const float top = max3(fmaxf(a0, a1), a2, a3);
+        const float top = max3(fmaxf(a0, a1), a2, a3) * c;
         // raise the maximum where the row is beyond it by 2^15 (or had none)
-        const bool raise = top > m && !((top - m) * c <= 15.0f);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float alpha = raise ? (m == -INFINITY ? 0.0f : fast_exp2((m - top) * c)) : 1.0f;
+        const bool raise = top > m && !(top - m <= 15.0f);
+        if (__any_sync(0xffffffffu, raise) || to != unit) {
+          float alpha = raise ? (m == -INFINITY ? 0.0f : fast_exp2(m - top)) : 1.0f;
           if (raise) m = top;
           l2.x *= alpha;
           l2.y *= alpha;
+          alpha *= exp2i(unit - to);
+          unit = to;
           if (j > 0) {
             // S of this step was issued after P V of the last and is complete, so O is at rest. The
             // scores are read again after it: their registers serve here.
@@ -647,7 +801,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           }
         }
         const float mu = m == -INFINITY ? 0.0f : m;
-        const float2 c2 = make_float2(c, c), n2 = make_float2(-mu * c, -mu * c);
+        const float2 c2 = make_float2(c, c), n2 = make_float2(-mu, -mu);
         float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
         for (int i = 0; i < kKeys; i += 32) {
@@ -671,16 +825,14 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         if (lane == 0) mbar_arrive(&bars->p_full[w]);
         l2 = __fadd2_rn(l2, __fadd2_rn(sum0, sum1));
       }
-      if (ok && n_steps > 0) ok = warp_wait(&bars->o_full[w], 0, abort, p.status, kStOFull);
+      if (ok) ok = warp_wait(&bars->o_full[w], 0, abort, p.status, kStOFull);
       if (ok) {
         tc_fence_after();
         const int r = tr;
         const bool live = r < rows;
         const int64_t row = my_row;
         const float L = l2.x + l2.y;
-        const float mz = m == -INFINITY ? -INFINITY : m * c;
-        const float unit = exp2i(v_top - 6);
-        const float inv = whole ? (L != 0.0f ? unit / L : 0.0f) : unit;
+        const float inv = whole ? (L != 0.0f ? exp2i(unit) / L : 0.0f) : exp2i(unit);
         const bool nans = bars->nans != 0;
         auto show_nans = [&](uint32_t* o, int col) {
 #pragma unroll
@@ -695,13 +847,8 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
           for (int i = 0; i < D; i += 32) {
             uint32_t o[32];
-            if (n_steps > 0) {
-              tmem_ld32(t_o + uint32_t(i), o);
-              tmem_wait_ld();
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0u;
-            }
+            tmem_ld32(t_o + uint32_t(i), o);
+            tmem_wait_ld();
             if (nans) show_nans(o, i);
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
@@ -760,10 +907,10 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           }
         }
         if (live && whole) {
-          if (p.lse != nullptr) p.lse[row] = L != 0.0f ? (mz + log2f(L)) * kLn2 : -INFINITY;
+          if (p.lse != nullptr) p.lse[row] = L != 0.0f ? (m + log2f(L)) * kLn2 : -INFINITY;
         } else if (live) {
           float* dst = p.ws + (row * p.ws_splits + split) * (D + 4) + D;
-          dst[0] = mz;
+          dst[0] = m;
           dst[1] = L;
         }
       }

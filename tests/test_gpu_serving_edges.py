@@ -164,3 +164,81 @@ def test_nan_values_behind_a_row(new, ctx, G, longest, D, page):
             if 0 < back <= n:
                 at.append((b, s.lens[b] - back, "v", h, d))
     _check_nan_attention(_with_nans(s, at), torch.bfloat16, G, max_seq_len=longest)
+
+
+# ------------------------------------------------------------------------------------
+# pages far apart in size
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,ctx,G", [([2], [200], 4), ([100], [200], 1), ([90], [1500], 2)])
+def test_values_of_pages_far_apart(page, D, new, ctx, G):
+    """Pages of values 2^45 to 2^75 larger than those that carry the probability: before them, beside
+    them in the same step, and behind them, where some rows do not see them. The large pages' keys have
+    a score 25600 below the others' at least, so their probability is zero and the tolerance is that of
+    the others alone: their probabilities are equal, so nothing but roundings of 2^-11 and the sums."""
+    s = Setup(new, ctx, H=1, D=D, page=page, seed=80).fill()
+    pages = s.table[0, :-(-s.lens[0] // page)]
+    plus, minus = (osv.e4m3_encode(np.full((page, D), x)) for x in (100.0, -100.0))
+    for i, pg in enumerate(pages):
+        large = i % 4 == 2 or i == len(pages) - 1
+        s.k[pg, 0], s.ks[pg, 0] = (minus if large else plus), 127
+        s.v[pg, 0] = osv.e4m3_encode(s.rng.standard_normal((page, D)) * 50)
+        s.vs[pg, 0] = 127 + (30 + i % 10 if large else -36 + i % 22)
+    q = torch.full((new[0], G, D), 2.0, dtype=torch.bfloat16, device="cuda")
+    out, lse = s.cache().attention(q, *s.batch(), max_q_len=new[0], scale=1.0, return_lse=True)
+    ro, rl, info = osv.kv_attention(f64(q), s.k, s.ks, s.v, s.vs, s.cu, s.lens, s.table, 1.0, True)
+    assert np.abs(ro).max() < 100 and info["vmax"].max() > 2.0 ** 30
+    tol = (2.0 ** -10 + (s.lens[0] + 66) * 2.0 ** -23) * info["pv"] + 2.0 ** -8 * np.abs(ro)
+    assert np.all(np.abs(f64(out) - ro) <= tol)
+    assert np.all(np.abs(f64(lse) - rl) <= 2.0 ** -18 + 2.0 ** -22 * np.abs(rl))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("new,ctx,G", [([2], [200], 4), ([100], [200], 1), ([90], [1500], 2)])
+def test_keys_of_pages_far_apart(page, new, ctx, G):
+    """Keys of 2^-30 to 2^-14 that carry the probability beside keys of 2^10 and more whose scores are
+    hugely negative: the small keys' scores differ and have to keep their bits."""
+    D = 64
+    s = Setup(new, ctx, H=1, D=D, page=page, seed=81).fill()
+    pages = s.table[0, :-(-s.lens[0] // page)]
+    small = np.zeros(len(pages) * page, dtype=bool)
+    for i, pg in enumerate(pages):
+        large = i % 4 == 2 or i == len(pages) - 1
+        small[i * page:(i + 1) * page] = not large
+        x = s.rng.standard_normal((page, D)) * 100
+        s.k[pg, 0] = osv.e4m3_encode(-np.abs(x) if large else x)
+        s.ks[pg, 0] = 127 + (6 + i % 20 if large else -30 + i % 8)
+    small = small[:s.lens[0]]
+    rng = np.random.default_rng(1)
+    q = torch.from_numpy(2.0 ** 20 * (1 + rng.random((new[0], G, D)))).to(torch.bfloat16).cuda()  # positive
+    scale = 2.0 ** -3
+    out, lse = s.cache().attention(q, *s.batch(), max_q_len=new[0], scale=scale, return_lse=True)
+    ro, rl, info = osv.kv_attention(f64(q), s.k, s.ks, s.v, s.vs, s.cu, s.lens, s.table, scale, True)
+    k = osv.kv_values(s.k, s.ks, s.table[0], s.lens[0])[:, 0]
+    z = scale * np.einsum("tgd,jd->tgj", f64(q), k)
+    assert z[:, :, ~small].max() < -2.0 ** 20 and 0.5 < z[:, :, small].max() < 100  # and they do differ
+    a = scale * np.einsum("tgd,jd->tgj", np.abs(f64(q)), np.abs(k[small])).max()
+    e = (D * 2.0 ** -23 + 2.0 ** -21) * a
+    n = s.lens[0]
+    assert np.all(np.abs(f64(lse) - rl) <= e + (n + 64) * 2.0 ** -23 + 2.0 ** -22 * (1 + np.abs(rl)))
+    tol = (2 * e + 2.0 ** -11 + (n + 66) * 2.0 ** -23) * info["pv"] + n * 2.0 ** -25 * info["vmax"][..., None]
+    assert np.all(np.abs(f64(out) - ro) <= tol + 2.0 ** -8 * np.abs(ro))
+
+
+def test_units_of_pages_change_often():
+    """Pages of every size of the whole range, in steps of 16 and of 128 keys: each row against the
+    largest product of probability and value that it sees (the sums are float32)."""
+    for page, D in ((16, 64), (128, 128), (32, 128)):
+        s = Setup([150, 70], [900, 0], H=2, D=D, page=page, seed=82).fill()
+        s.vs[:] = 127 + s.rng.integers(-40, 41, s.vs.shape)
+        s.ks[:] = np.minimum(s.ks, 122) - s.rng.integers(0, 30, s.ks.shape)
+        q = torch.randn(220, 2, D, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+        cache = s.cache()
+        out, lse = cache.attention(q, *s.batch(), max_q_len=150, scale=0.125, return_lse=True)
+        assert cache.device_status() == 0
+        ro, rl, info = osv.kv_attention(f64(q), s.k, s.ks, s.v, s.vs, s.cu, s.lens, s.table, 0.125, True)
+        n = max(s.lens)
+        e = ((D * 2.0 ** -23 + 2.0 ** -21) * info["a"])[..., None]
+        tol = (2 * e + 2.0 ** -11 + (n + 66) * 2.0 ** -23) * info["pv"] + n * 2.0 ** -25 * info["vmax"][..., None]
+        assert np.all(np.abs(f64(out) - ro) <= tol + 2.0 ** -8 * np.abs(ro))
