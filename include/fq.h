@@ -278,7 +278,8 @@ FQ_API fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch
  *               two streams, or two captured graphs) need one each
  * Sums, maxima and the softmax are float32. Keys and values enter the products exactly (an E4M3
  * code is an fp16 number), queries too, scaled by a power of two per row, but for elements 2^-29
- * below the row's largest; the probabilities are rounded to fp16 for the second product. The scales
+ * below the row's largest; the probabilities are rounded to fp16 for the second product: by 2^-11, or by
+ * 2^-37 of the row's largest where they are below 2^-26 of it. The scales
  * of the pages may lie as far apart as their range allows. A NaN code makes the outputs NaN of the
  * rows that see its token: a key's whole rows and their lse, a value's element. Scores past the
  * float32 range and NaN in q are outside the contract.

@@ -25,7 +25,8 @@
 // of q is scaled by the power of two that brings its largest magnitude into [2^14, 2^15) and
 // converted to fp16: exact but for elements 2^-29 below the largest. The products are then exact in
 // the fp32 sums of mma.sync, and the powers of two (q row, page of k) are applied to the score in
-// float32. Probabilities are rounded to fp16 (2^-11) for the second product. The output accumulates
+// float32. Probabilities are taken times 2^15 and rounded to fp16 for the second product: by 2^-11, or
+// 2^-40 of the row's largest where they are below 2^-29 of it. The output accumulates
 // in units of the page's own scale of v and moves to the next page's unit by a power of two, so that
 // no page's scale has to fit beside another's in fp16: exponents lie in [-40, 40], so a unit changes
 // by at most 2^80 and float32 holds all of it.
@@ -42,6 +43,7 @@ using namespace kv;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kMaxChunkBytes = 4096 * 128;  // of K in one chunk (V as much again)
 constexpr int kMaxCluster = 8;              // chunks that are joined in a cluster, at most
+constexpr float kHeadroom = 15.0f;          // the largest probability is 2^15 before it is divided by the sum
 
 enum : uint32_t { kStFull = 1u << 0 };
 
@@ -396,7 +398,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         mt_max = fmaxf(mt_max, __shfl_xor_sync(0xffffffffu, mt_max, 4));
         mt_max = fmaxf(mt_max, __shfl_xor_sync(0xffffffffu, mt_max, 8));
         mt_max = fmaxf(mt_max, __shfl_xor_sync(0xffffffffu, mt_max, 16));
-        const float mn = fmaxf(m[n][e], mt_max);
+        const float mn = fmaxf(m[n][e], mt_max - kHeadroom);
         mu[n][e] = mn == -INFINITY ? 0.0f : mn;  // a row that has seen nothing yet
         alpha[n][e] = fast_exp2(m[n][e] - mu[n][e]);
         m[n][e] = mn;

@@ -20,10 +20,12 @@
 // beside the softmax: with the units of every step worked out in every CTA the 8192-token prompt took
 // 607 us, now 551.)
 //
-// Softmax. A thread owns one row (its TMEM lane), so no exchange is needed. The maximum that the
-// exponents are taken against is only raised when a row exceeds it by 2^15 (the probabilities then
-// stay below 2^15, within fp16, and relative rounding is the same): O and the sum are rescaled that
-// rarely. Probabilities are rounded to fp16 (2^-11).
+// Softmax. A thread owns one row (its TMEM lane), so no exchange is needed. What the exponents are taken
+// against is only raised when a probability would pass 2^15.9 (within fp16); O and the sum are rescaled
+// then. It is set so that the largest score has probability 2^12: the rounding to fp16 is 2^-11 of a
+// probability, or 2^-37 of the row's largest for those below 2^-26 of it. (8192-token prompt: 552 us with 2^0
+// for 2^12, where probabilities below 2^-14 of the largest lose bits and below 2^-25 vanish from O but not
+// from the sum; 562 with 2^8, 573 with 2^14.)
 //
 // Roles, 512 threads: warp 0 MMA issuer (owns TMEM), 1 TMA producer, 4-7 and 8-11 softmax of row
 // tile 0 and 1 (its Q before, its output after), 12-15 converters. The issuer comes first and waits as
@@ -59,6 +61,9 @@ enum : uint32_t {
 constexpr uint32_t kAllThere = (1u << (kKeys / 16)) - 1u;  // a step with all its pages
 constexpr uint32_t kChange = 1u << 31, kLast = 1u << 30;
 constexpr int kNoPage = -1000;  // no exponent
+// Probabilities are taken times 2^kBase for a row's largest score when its reference was set, and the
+// reference is set anew when one passes 2^kMost (fp16 ends at 2^16)
+constexpr float kBase = 12.0f, kMost = 15.9f;
 
 template <int D>
 struct Geo {
@@ -729,7 +734,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       if (p.causal) v = min(v, s.len - s.n + i0 + int64_t(ti) + 1);
       vis = tr < rows ? int(max(min(v - c0, int64_t(keys)), int64_t(0))) : 0;
     }
-    float m = -INFINITY;  // the row's maximum that the exponents are taken against (of z log2 e = S * c)
+    float m = -INFINITY;  // what the row's exponents are taken against (of z log2 e = S * c)
     int unit = 0;         // of O
     int ahead = 0;        // vis, less what the step's first key is beyond j * kKeys
     float2 l2 = make_float2(0.0f, 0.0f);
@@ -775,11 +780,11 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         a0 = max3(a0, x[kKeys - 4], x[kKeys - 3]);
         a1 = max3(a1, x[kKeys - 2], x[kKeys - 1]);
         const float top = max3(fmaxf(a0, a1), a2, a3) * c;
-        // raise the maximum where the row is beyond it by 2^15 (or had none)
-        const bool raise = top > m && !(top - m <= 15.0f);
+        // raise the reference where the row is beyond it by 2^kMost (or had none)
+        const bool raise = top > m && !(top - m <= kMost);
         if (__any_sync(0xffffffffu, raise) || to != unit) {
-          float alpha = raise ? (m == -INFINITY ? 0.0f : fast_exp2(m - top)) : 1.0f;
-          if (raise) m = top;
+          float alpha = raise ? (m == -INFINITY ? 0.0f : fast_exp2(m - (top - kBase))) : 1.0f;
+          if (raise) m = top - kBase;
           l2.x *= alpha;
           l2.y *= alpha;
           alpha *= exp2i(unit - to);

@@ -242,3 +242,35 @@ def test_units_of_pages_change_often():
         e = ((D * 2.0 ** -23 + 2.0 ** -21) * info["a"])[..., None]
         tol = (2 * e + 2.0 ** -11 + (n + 66) * 2.0 ** -23) * info["pv"] + n * 2.0 ** -25 * info["vmax"][..., None]
         assert np.all(np.abs(f64(out) - ro) <= tol + 2.0 ** -8 * np.abs(ro))
+
+
+# ------------------------------------------------------------------------------------
+# probabilities far below the largest
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("new,ctx,G,longest", [
+    ([1], [3000], 4, None), ([1], [3000], 4, 60000), ([3], [200], 2, None),  # one chunk, a cluster's, the workspace's
+    ([100], [3000], 1, None), ([300], [20], 2, None)])                       # prompts
+@pytest.mark.parametrize("gap", [16, 24])
+def test_a_dominating_key_without_value(new, ctx, G, longest, gap):
+    """One key holds all but a few millionths of the probability and its value is zero: the output is the
+    others'. With a gap of 16 +- 1 (2^-24.6) every probability is rounded by 2^-11, so the tolerance is
+    relative to the others; with 24 (2^-36.1) 2^-37 of the largest is added."""
+    D, page = 64, 64
+    s = Setup(new, ctx, H=1, D=D, page=page, seed=90, width=-(-(longest or 4000) // page)).fill()
+    pages = s.table[0, :-(-s.lens[0] // page)]
+    for pg in pages:
+        s.k[pg, 0] = osv.e4m3_encode(s.rng.uniform(-1.0, 1.0, (page, D)) / 32)  # scores of at most 1 beside q = 1
+        s.v[pg, 0] = osv.e4m3_encode(1.0 + s.rng.uniform(0.0, 1.0, (page, D)))
+        s.ks[pg, 0] = s.vs[pg, 0] = 127
+    s.k[pages[0], 0, 0], s.v[pages[0], 0, 0] = osv.e4m3_encode(np.full(D, gap / D)), 0
+    n = new[0]
+    q = torch.full((n, G, D), 0.5, dtype=torch.bfloat16, device="cuda")
+    out, lse = s.cache().attention(q, *s.batch(), max_q_len=n, max_seq_len=longest or s.lens[0], scale=2.0, return_lse=True)
+    ro, rl, info = osv.kv_attention(f64(q), s.k, s.ks, s.v, s.vs, s.cu, s.lens, s.table, 2.0, True)
+    e = ((D * 2.0 ** -23 + 2.0 ** -21) * info["a"])[..., None]
+    tol = (2 * e + 2.0 ** -11 + (s.lens[0] + 66) * 2.0 ** -23) * info["pv"] + 2.0 ** -8 * np.abs(ro)
+    if gap > 17:
+        tol += s.lens[0] * 2.0 ** -37 * info["vmax"][..., None]
+    assert 0 < np.abs(ro).max() < 2.0 ** -10
+    assert np.all(np.abs(f64(out) - ro) <= tol), float((np.abs(f64(out) - ro) / tol).max())
+    assert np.all(np.abs(f64(lse) - rl) <= e[..., 0] + (s.lens[0] + 64) * 2.0 ** -23 + 2.0 ** -22 * (1 + np.abs(rl)))
