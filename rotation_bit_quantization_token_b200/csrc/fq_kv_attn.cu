@@ -157,8 +157,8 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   if (tid == 0 && split == 0 && h == 0 && tile == 0 && p.status != nullptr && (!s.ok || s.n > p.max_q_len))
     atomicOr(p.status, FQ_KV_BAD_BATCH);
   const int row0 = tile * kRowsTile;
-  const int rows = int(min(int64_t(kRowsTile), s.n * G - row0));
-  if (rows <= 0 || takes_tc(p, s.n, G)) return;
+  const int rows = int(min(int64_t(kRowsTile), s.q * G - row0));
+  if (rows <= 0 || takes_tc(p, s.q, G)) return;
   const int64_t c0 = int64_t(split) * p.chunk;  // first key of the chunk
   if (c0 >= s.end && split > 0) return;
   const int keys = int(min(int64_t(p.chunk), s.end - c0));
@@ -653,10 +653,10 @@ kv_attn_join_kernel(const KvAttnParams p, const int few) {
   }
   const int64_t i = t - __ldg(p.b.cu_new + lo);
   const int64_t n_new = int64_t(__ldg(p.b.cu_new + lo + 1)) - __ldg(p.b.cu_new + lo);
-  const bool tc = takes_tc(p, n_new, G);
+  const bool tc = takes_tc(p, min(n_new, int64_t(p.max_q_len)), G);
   const int tile_rows = tc ? kTcRows : p.tile_rows, chunk = tc ? p.tc_chunk : p.chunk;
   const Rows s = sequence_rows(p, lo, (i * G + hq % G) / tile_rows * tile_rows, tile_rows, G);
-  live = live && i >= 0 && i < s.n && i < p.max_q_len && s.end > chunk && (tc || !p.cluster);
+  live = live && i >= 0 && i < s.q && s.end > chunk && (tc || !p.cluster);
   // every thread waits, also where there is nothing to do: this kernel must not end before the
   // attention does, or what comes after it could start beside that
   grid_dependency_wait();

@@ -290,8 +290,8 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const Rows s = sequence_rows(p, b, row0, kTcRows, G);
   if (tid == 0 && split == 0 && h == 0 && tile == 0 && p.status != nullptr && (!s.ok || s.n > p.max_q_len))
     atomicOr(p.status, FQ_KV_BAD_BATCH);
-  const int rows = int(min(int64_t(kTcRows), s.n * G - row0));
-  if (rows <= 0 || !takes_tc(p, s.n, G)) return;
+  const int rows = int(min(int64_t(kTcRows), s.q * G - row0));
+  if (rows <= 0 || !takes_tc(p, s.q, G)) return;
   const int64_t c0 = int64_t(split) * p.tc_chunk;
   if (c0 >= s.end && split > 0) return;
   const int keys = int(min(int64_t(p.tc_chunk), s.end - c0));

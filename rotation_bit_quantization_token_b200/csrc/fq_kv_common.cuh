@@ -58,6 +58,7 @@ __device__ __forceinline__ int page_exp(uint32_t byte) {
 struct Rows {
   int64_t t_first;  // first token row of the sequence
   int64_t n, len;   // new tokens, length
+  int64_t q;        // new tokens whose queries are computed: the first max_q_len
   int64_t end;      // keys seen by at least one of the rows
   bool ok;
 };
@@ -73,7 +74,8 @@ __device__ __forceinline__ Rows sequence_rows(const KvAttnParams& p, int b, int6
   r.ok = r.n >= 0 && r.t_first >= 0 && r.t_first + r.n <= p.T;
   r.ok = r.ok && r.len >= 0 && r.len <= p.max_seq_len && r.n <= r.len;
   if (!r.ok) r.n = 0;
-  const int64_t last = min(quotient(row0 + count - 1, G), r.n - 1);
+  r.q = min(r.n, int64_t(p.max_q_len));
+  const int64_t last = min(quotient(row0 + count - 1, G), r.q - 1);
   r.end = p.causal ? min(r.len, r.len - r.n + last + 1) : r.len;
   if (r.end < 0) r.end = 0;
   return r;
@@ -101,9 +103,9 @@ __device__ __forceinline__ void hide_nans(uint4& v, int key, int d0, int* nan_fr
   }
 }
 
-// Whether the tensor-core kernel takes a sequence with n new tokens (else the other one does):
+// Whether the tensor-core kernel takes a sequence with q tokens' queries (else the other one does):
 // more than p.tc_rows rows. Both kernels and the join decide by it.
-__device__ __forceinline__ bool takes_tc(const KvAttnParams& p, int64_t n, int G) { return n * G > p.tc_rows; }
+__device__ __forceinline__ bool takes_tc(const KvAttnParams& p, int64_t q, int G) { return q * G > p.tc_rows; }
 
 }  // namespace kv
 }  // namespace fq

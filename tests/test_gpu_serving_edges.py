@@ -274,3 +274,35 @@ def test_a_dominating_key_without_value(new, ctx, G, longest, gap):
     assert 0 < np.abs(ro).max() < 2.0 ** -10
     assert np.all(np.abs(f64(out) - ro) <= tol), float((np.abs(f64(out) - ro) / tol).max())
     assert np.all(np.abs(f64(lse) - rl) <= e[..., 0] + (s.lens[0] + 64) * 2.0 ** -23 + 2.0 ** -22 * (1 + np.abs(rl)))
+
+
+# ------------------------------------------------------------------------------------
+# bounds of a call that its batch passes
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("new,ctx,G,bound", [
+    ([100], [30], 1, 64), ([100, 3, 90], [30, 200, 0], 1, 64),  # the call's rows fit the one kernel, the sequences' do not
+    ([300, 20], [10, 700], 2, 130), ([300], [2000], 1, 80),     # prompts, whole and in chunks
+    ([20, 3], [600, 2500], 4, 1), ([20, 3], [600, 2500], 4, 2), ([9], [40], 3, 5)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_new_tokens_than_max_q_len(new, ctx, G, bound, causal):
+    """The first max_q_len queries of a longer sequence are computed, the others' rows are not written,
+    and the batch is reported."""
+    s = Setup(new, ctx, H=2, D=64, page=32, seed=91).fill()
+    n, Hq = s.cu[-1], 2 * G
+    q = torch.randn(n, Hq, 64, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).cuda()
+    cache = s.cache()
+    out = torch.full((n, Hq, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n, Hq), 9.0, device="cuda")
+    cache.attention(q, *s.batch(), max_q_len=bound, max_seq_len=max(s.lens), causal=causal, out=out, lse=lse, return_lse=True)
+    assert cache.device_status() == _lib.FQ_KV_BAD_BATCH
+    index = np.concatenate([np.arange(c) for c in new])
+    done, left = index < bound, torch.from_numpy(index >= bound).cuda()
+    assert bool((out[left] == 9.0).all()) and bool((lse[left] == 9.0).all())
+    ro, rl, info = osv.kv_attention(f64(q), s.k, s.ks, s.v, s.vs, s.cu, s.lens, s.table, 0.125, causal)
+    keys = max(s.lens)
+    e = (64 * 2.0 ** -23 + 2.0 ** -21) * info["a"]
+    tol = ((2 * e + 2.0 ** -11 + (keys + 66) * 2.0 ** -23)[..., None] * info["pv"]
+           + keys * 2.0 ** -25 * info["vmax"][..., None] + 2.0 ** -8 * np.abs(ro))
+    assert np.all((np.abs(f64(out) - ro) <= tol)[done])
+    ltol = e + (keys + 64) * 2.0 ** -23 + 2.0 ** -22 * (1 + np.abs(rl))
+    assert np.all((np.abs(f64(lse) - rl) <= ltol)[done])
