@@ -217,9 +217,9 @@ typedef struct {
  *               page_table[b, j]; entries past a sequence's last page are not read
  * num_seqs in [1, 65536], table_width in [1, 2^24].
  * Contents that are out of range are refused on the device, and FQ_KV_BAD_BATCH is set in the
- * call's status word: a sequence with more new tokens than its length, or rows outside [0, T),
- * or (attention) a length past max_seq_len gets neither pages nor outputs written; a token whose
- * page lies outside the table or the cache is not stored, and not attended to. */
+ * call's status word: a sequence with more new tokens than its length, fewer than none, or rows
+ * outside [0, T), or (attention) a length past max_seq_len gets neither pages nor outputs written; a
+ * token whose page lies outside the table or the cache is not stored, and not attended to. */
 typedef struct {
     const int32_t *cu_new, *seq_lens, *page_table;
     int32_t num_seqs, table_width;

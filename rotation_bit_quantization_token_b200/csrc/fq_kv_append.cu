@@ -198,19 +198,28 @@ kv_append_kernel(const KvAppendParams p, const unsigned kv_ctas, const unsigned 
   const int H = p.c.kv_heads;
   const int ps_log = 31 - __clz(p.c.page_size), ps = 1 << ps_log;
 
+  // The first CTAs look after a sequence each and report it if its batch entries are out of range (its own
+  // items may not be found then). There are two CTAs a sequence at least.
+  const bool checks = blockIdx.x < unsigned(p.b.num_seqs) && p.status != nullptr;
+  int c_first = 0, c_end = 0, c_len = 0;
+  if (checks) {
+    c_first = __ldg(p.b.cu_new + blockIdx.x);
+    c_end = __ldg(p.b.cu_new + blockIdx.x + 1);
+    c_len = __ldg(p.b.seq_lens + blockIdx.x);
+  }
+
   // ---- the work item: the last sequence with start(b) <= item ----
   const int item = int(blockIdx.x / groups), group = int(blockIdx.x - unsigned(item) * groups);
   const int b = warp_search(p.b.num_seqs, item, [&](int i) { return (__ldg(p.b.cu_new + i) >> ps_log) + 2 * i; });
   const int64_t t_first = __ldg(p.b.cu_new + b);
   const int64_t n = int64_t(__ldg(p.b.cu_new + b + 1)) - t_first;
   const int64_t len = __ldg(p.b.seq_lens + b);
+  if (checks && tid == 0 && (c_first < 0 || c_end < c_first || c_end > p.T || int64_t(c_end) - c_first > c_len))
+    atomicOr(p.status, FQ_KV_BAD_BATCH);
   const int64_t first = len - n;  // position of the first new token
   const int64_t local = int64_t(item) - ((t_first >> ps_log) + 2 * int64_t(b));
   if (n <= 0 || local < 0) return;
-  if (first < 0 || t_first < 0 || t_first + n > p.T) {
-    if (tid == 0 && p.status != nullptr) atomicOr(p.status, FQ_KV_BAD_BATCH);
-    return;
-  }
+  if (first < 0 || t_first < 0 || t_first + n > p.T) return;
   const int64_t page_idx = (first >> ps_log) + local;
   const int64_t at0 = page_idx << ps_log;
   if (at0 >= len) return;

@@ -12,7 +12,7 @@ import torch
 
 from oracle import serving as osv
 from test_gpu_kv import HALF, Setup, f64
-from rotation_bit_quantization_token_b200 import _lib, int8_matmul
+from rotation_bit_quantization_token_b200 import KVCache, _lib, int8_matmul
 
 pytestmark = pytest.mark.gpu
 
@@ -306,3 +306,23 @@ def test_more_new_tokens_than_max_q_len(new, ctx, G, bound, causal):
     assert np.all((np.abs(f64(out) - ro) <= tol)[done])
     ltol = e + (keys + 64) * 2.0 ** -23 + 2.0 ** -22 * (1 + np.abs(rl))
     assert np.all((np.abs(f64(lse) - rl) <= ltol)[done])
+
+
+@pytest.mark.parametrize("cu,lens", [
+    ([0, 3, 1, 5], [9, 9, 9]),         # fewer new tokens than none
+    ([0, 5, 5, 4], [9, 9, 9]), ([0, 2, 2, 7], [9, 9, 9]), ([40, 41, 41, 41], [9, 9, 9]), ([0, 2, 2, 2000000000], [9, 9, 9]),
+    ([-3, -2, 0, 5], [9, 9, 9]), ([0, 2, 5, 5], [9, 2, 9]), ([0, 2, 2, 5], [9, -1, 9])])
+def test_batches_out_of_range_are_reported(cu, lens):
+    """Both calls report a batch whose rows fall, end behind the arrays or begin there, or whose lengths
+    are shorter than the new tokens."""
+    cache = KVCache(6, 16, 1, 64)
+    x = torch.randn(5, 1, 64, device="cuda").half()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = i32([[0], [1], [2]])
+    cache.append(x, x, i32(cu), i32(lens), table, q=x, inv_freq=torch.ones(16, device="cuda"))
+    assert cache.device_status() == _lib.FQ_KV_BAD_BATCH
+    cache.attention(x, i32(cu), i32(lens), table, max_q_len=5)
+    assert cache.device_status() == _lib.FQ_KV_BAD_BATCH
+    cache.append(x, x, i32([0, 2, 2, 5]), i32([2, 0, 4]), table)
+    cache.attention(x, i32([0, 2, 2, 5]), i32([2, 0, 4]), table, max_q_len=3)
+    assert cache.device_status() == 0
