@@ -169,13 +169,21 @@ FQ_API fq_status fq_mx_matmul(int64_t T, int64_t O, int64_t L, const void *a_fp4
  *   a, w       [T, L] and [O, L] int8, 16-byte aligned
  *   out_type   FQ_BF16, FQ_FP16 or FQ_FP32: the type of C [T, O], row-major, aligned to its
  *              elements
- *   status     a device word, or NULL: as in fq_mx_matmul
+ *   status     a device word, ORed with a nonzero code if a bounded wait inside the kernel gives
+ *              up (the output is then undefined), or NULL: a word that the library keeps on each
+ *              device, which fq_int8_device_status reads
  * Allocates nothing; asynchronous on stream. Errors: FQ_ERR_NULLPTR (a, a_scale, w, w_scale,
  * C), FQ_ERR_INVALID (a size or type out of range, L % 16 != 0, misaligned pointer),
  * FQ_ERR_CUDA. */
 FQ_API fq_status fq_int8_matmul(int64_t T, int64_t O, int64_t L, const int8_t* a, const float* a_scale,
                                 const int8_t* w, const float* w_scale, fq_dtype out_type, void* C,
                                 uint32_t* status, struct CUstream_st* stream);
+
+/* Reads and clears the current device's status word of the fq_int8_matmul calls that were given
+ * none. *status = 0 when none of them gave up a bounded wait since the last read, else a nonzero
+ * code (and the call returns FQ_ERR_DEVICE_TIMEOUT). Synchronizes the device. Returns
+ * FQ_ERR_NULLPTR for a NULL status, FQ_ERR_CUDA if the copy fails. */
+FQ_API fq_status fq_int8_device_status(uint32_t *status);
 
 /* Test hook for the failure path of fq_int8_matmul: process-wide and one-shot, like
  * fq_static_debug_arm_stall. In the next call one CTA of every cluster (every CTA where none is

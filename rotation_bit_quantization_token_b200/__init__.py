@@ -9,6 +9,6 @@ with INT8 weights (int8_matmul), and a paged key / value cache in E4M3 with rota
 and attention over it (KVCache).
 """
 
-from .api import (FlatQuant, HostPipeline, KVCache, debug_rotate, int8_matmul,  # noqa: F401
+from .api import (FlatQuant, HostPipeline, KVCache, debug_rotate, int8_device_status, int8_matmul,  # noqa: F401
                   quantize_mx, quantize_mx_static, quantize_per_token)
 from ._lib import FQError, load as load_library  # noqa: F401

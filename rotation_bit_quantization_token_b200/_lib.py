@@ -51,6 +51,7 @@ _SIGNATURES = {
     "fq_quantize_mx_static": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _dbl, _vp, _vp, _vp]),
     "fq_mx_matmul": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fq_int8_matmul": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp]),
+    "fq_int8_device_status": (_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "fq_int8_debug_arm_stall": (_int, [_dbl]),
     "fq_kv_append": (_int, [_cache_p, _batch_p, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i32, _int,
                             _vp, _i64, _i32, _vp, _vp, _vp]),

@@ -283,7 +283,8 @@ def int8_matmul(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stat
     with float32 scales (see fq_int8_matmul): a and a_scale as quantize_per_token gives them
     with out_dtype="int8", w and w_scale alike for the weights' rows. out_dtype bfloat16,
     float16 or float32. status: an int32 tensor of one element, ORed with a nonzero code if a
-    bounded wait inside the kernel gives up (the output is then undefined)."""
+    bounded wait inside the kernel gives up (the output is then undefined); without it
+    int8_device_status() tells."""
     lib = _lib.load()
     dev = torch.cuda.current_device() if isinstance(a, torch.Tensor) and a.is_cuda else -1
     if not (dev >= 0 and _fits(a, torch.int8, dev) and _fits(a_scale, torch.float32, dev) and _fits(w, torch.int8, dev)
@@ -314,6 +315,16 @@ def int8_matmul(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stat
     if st != _lib.FQ_OK:
         _lib.check(st, "fq_int8_matmul")
     return out
+
+
+def int8_device_status():
+    """Reads and clears the current device's status word of int8_matmul calls without one of their
+    own: 0, or the bits of bounded waits that gave up since. Synchronizes the device."""
+    v = ctypes.c_uint32(0)
+    st = _lib.load().fq_int8_device_status(ctypes.byref(v))
+    if st not in (_lib.FQ_OK, _lib.FQ_ERR_DEVICE_TIMEOUT):
+        _lib.check(st, "fq_int8_device_status")
+    return int(v.value)
 
 
 class KVCache:

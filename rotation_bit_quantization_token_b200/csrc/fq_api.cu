@@ -233,6 +233,19 @@ fq_status fq_int8_matmul(int64_t T, int64_t O, int64_t L, const int8_t* a, const
   return e == cudaSuccess ? FQ_OK : cuda_fail(e);
 }
 
+fq_status fq_int8_device_status(uint32_t* status) {
+  if (status == nullptr) return FQ_ERR_NULLPTR;
+  uint32_t* word = nullptr;
+  uint32_t v = 0;
+  cudaError_t e = fq::i8gemm_status_word(&word);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&v, word, sizeof(v), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && v != 0) e = cudaMemset(word, 0, sizeof(v));
+  if (e != cudaSuccess) return cuda_fail(e);
+  *status = v;
+  return v != 0 ? FQ_ERR_DEVICE_TIMEOUT : FQ_OK;
+}
+
 fq_status fq_int8_debug_arm_stall(double wait_limit_s) {
   if (!(wait_limit_s > 0.0 && wait_limit_s <= 10.0)) return FQ_ERR_INVALID;
   g_int8_stall_ns.store(uint64_t(wait_limit_s * 1e9));

@@ -78,12 +78,13 @@ struct I8GemmParams {
   const void* w;         // [O, L] int8
   const float* w_scale;  // [O]
   void* C;               // [T, O] of out_type
-  uint32_t* status;      // bounded-wait status word, or nullptr
+  uint32_t* status;      // bounded-wait status word, or nullptr: the library's own
   int64_t T, O, L;
   fq_dtype out_type;
   uint64_t stall_ns;     // test hook (fq_int8_debug_arm_stall): 0 = off, else the wait limit
 };
 cudaError_t launch_i8gemm(const I8GemmParams& p, int num_sms, cudaStream_t stream);
+cudaError_t i8gemm_status_word(uint32_t** word);  // of calls without one, on the current device
 
 // Keeps a CUDA error code for fq_last_cuda_error() (thread-local).
 void record_cuda_error(int e);

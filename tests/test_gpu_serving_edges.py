@@ -12,7 +12,7 @@ import torch
 
 from oracle import serving as osv
 from test_gpu_kv import HALF, Setup, f64
-from rotation_bit_quantization_token_b200 import KVCache, _lib, int8_matmul
+from rotation_bit_quantization_token_b200 import KVCache, _lib, int8_device_status, int8_matmul
 
 pytestmark = pytest.mark.gpu
 
@@ -76,6 +76,19 @@ def test_product_whose_waits_run_out(T, O, L):
 def test_pairs_whose_waits_run_out(T, O, L):
     """Pairs of CTAs: fewer stages than the ring holds, several tiles, long rows."""
     _product_gives_up(T, O, L)
+
+
+@pytest.mark.parametrize("T,O,L", [(3, 130, 144), (5, 128, 8192), (2049, 2056, 4096)])
+def test_waits_that_run_out_are_kept_without_a_status_tensor(T, O, L):
+    a, w = (torch.ones(n, L, dtype=torch.int8, device="cuda") for n in (T, O))
+    sa, sw = (torch.ones(n, device="cuda") for n in (T, O))
+    int8_matmul(a, sa, w, sw)
+    assert int8_device_status() == 0
+    assert _lib.load().fq_int8_debug_arm_stall(0.05) == _lib.FQ_OK
+    int8_matmul(a, sa, w, sw)
+    assert int8_device_status() != 0 and int8_device_status() == 0
+    assert torch.all(int8_matmul(a, sa, w, sw, out_dtype=torch.float32) == L) and int8_device_status() == 0
+    assert _lib.load().fq_int8_device_status(None) == _lib.FQ_ERR_NULLPTR
 
 
 def test_product_stall_hook_checks_its_limit():
