@@ -385,10 +385,13 @@ class KVCache:
 
     def device_status(self):
         """Reads and clears the cache's status word: 0, or the bits that calls on this cache have
-        set since (FQ_KV_BAD_BATCH: a batch's contents were out of range). Synchronizes."""
+        set since (FQ_KV_BAD_BATCH: a batch's contents were out of range), on whatever stream.
+        Synchronizes the device."""
+        torch.cuda.synchronize(self._device)
         v = int(self._status.item())
         if v:
-            self._status.zero_()
+            self._status.bitwise_and_(~v)
+            torch.cuda.synchronize(self._device)  # a later call on another stream comes after it
         return v
 
     def _batch_desc(self, cu_new, seq_lens, page_table):

@@ -339,3 +339,26 @@ def test_batches_out_of_range_are_reported(cu, lens):
     cache.append(x, x, i32([0, 2, 2, 5]), i32([2, 0, 4]), table)
     cache.attention(x, i32([0, 2, 2, 5]), i32([2, 0, 4]), table, max_q_len=3)
     assert cache.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------
+# streams and threads
+# ------------------------------------------------------------------------------------
+def test_device_status_covers_other_streams():
+    """A bad batch queued on another stream behind a delay is reported, once."""
+    cache = KVCache(4, 16, 1, 64)
+    x = torch.randn(2, 1, 64, device="cuda").half()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    cu, good, bad, table, out = i32([0, 2]), i32([2]), i32([1]), i32([[0]]), torch.empty_like(x)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda n: cache.append(x, x, cu, n, table, stream=st),
+                 lambda n: cache.attention(x, cu, n, table, 2, out=out, stream=st)):
+        call(good)  # (the first call loads the kernel, which waits for the device)
+        assert cache.device_status() == 0
+        with torch.cuda.stream(st):
+            torch.cuda._sleep(40_000_000)  # about 20 ms
+        call(bad)
+        assert cache.device_status() == _lib.FQ_KV_BAD_BATCH
+        call(good)
+        assert cache.device_status() == 0
