@@ -3,6 +3,11 @@
 Every step of the operator runs in libfq's CUDA kernels; this module only checks
 tensor placement, allocates outputs with torch, and passes pointers and the current
 CUDA stream. There is no CPU implementation here.
+
+stream= takes another torch.cuda.Stream than the current one, for the kernels and for the
+outputs and workspaces that a call allocates: as with any tensor of another stream's memory,
+a caller who uses an output on the current stream lets that wait for `stream`, and calls
+record_stream on it before dropping it.
 """
 
 import ctypes
@@ -209,11 +214,11 @@ class FlatQuant:
         P2 = self._inputs(x, P1, P2, allow_no_p2=True)
         K, M, N = self.K, self.M, self.N
         if out is None:
-            out = torch.empty((K, M * N // 2), dtype=torch.uint8, device=x.device)
+            out = _empty(x, (K, M * N // 2), torch.uint8, stream)
         else:
             _check_output("out", out, K * M * N // 2, x.device)
         if scales is None:
-            scales = torch.empty((K, -(-M * N // 64), 2), dtype=torch.uint8, device=x.device)
+            scales = _empty(x, (K, -(-M * N // 64), 2), torch.uint8, stream)
         else:
             _check_output("scales", scales, _scale_bytes(K, M, N), x.device)
         _lib.check(self._lib.fq_quantize_mx(
@@ -225,7 +230,7 @@ class FlatQuant:
         """x'' = P1 . (x . P2) as float32 [K, M, N] (test hook)."""
         P2 = self._inputs(x, P1, P2, allow_no_p2=True)
         if out is None:
-            out = torch.empty((self.K, self.M, self.N), dtype=torch.float32, device=x.device)
+            out = _empty(x, (self.K, self.M, self.N), torch.float32, stream)
         else:
             _check_output("out", out, 4 * self.K * self.M * self.N, x.device, torch.float32)
         _lib.check(self._lib.fq_debug_rotate(self._h, _ptr(x), _ptr(P1), _ptr(P2), _ptr(out),
@@ -265,11 +270,11 @@ def quantize_mx_static(x, P1, P2, dst_type_max=0.0, out=None, scales=None, strea
         raise ValueError("P2 must be [N, N]")
     _check_device(x, P1=P1, P2=P2)
     if out is None:
-        out = torch.empty((K, M * N // 2), dtype=torch.uint8, device=x.device)
+        out = _empty(x, (K, M * N // 2), torch.uint8, stream)
     else:
         _check_output("out", out, K * M * N // 2, x.device)
     if scales is None:
-        scales = torch.empty((K, -(-M * N // 64), 2), dtype=torch.uint8, device=x.device)
+        scales = _empty(x, (K, -(-M * N // 64), 2), torch.uint8, stream)
     else:
         _check_output("scales", scales, _scale_bytes(K, M, N), x.device)
     _lib.check(lib.fq_quantize_mx_static(K, M, N, _DT[x.dtype], _ptr(x), _ptr(P1), _ptr(P2),

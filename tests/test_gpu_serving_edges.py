@@ -12,7 +12,7 @@ import torch
 
 from oracle import serving as osv
 from test_gpu_kv import HALF, Setup, f64
-from rotation_bit_quantization_token_b200 import KVCache, _lib, int8_device_status, int8_matmul
+from rotation_bit_quantization_token_b200 import FlatQuant, KVCache, _lib, int8_device_status, int8_matmul, quantize_mx_static
 
 pytestmark = pytest.mark.gpu
 
@@ -362,3 +362,28 @@ def test_device_status_covers_other_streams():
         assert cache.device_status() == _lib.FQ_KV_BAD_BATCH
         call(good)
         assert cache.device_status() == 0
+
+
+def test_memory_of_the_given_stream_in_every_mode():
+    """Outputs of the per-group calls and of the rotation alone, too, come from the given stream's memory:
+    not what the current stream has freed but still has to read."""
+    K, M, N = 32, 16, 16
+    x = torch.randn(K, M, N, device="cuda").to(torch.bfloat16)
+    eye = torch.eye(16, device="cuda").to(torch.bfloat16)
+    fq, st = FlatQuant(K, M, N), torch.cuda.Stream()
+    for call in (lambda: fq.quantize_mx(x, eye, eye, stream=st), lambda: quantize_mx_static(x, eye, eye, stream=st),
+                 lambda: (fq.debug_rotate(x, eye, eye, stream=st),),
+                 lambda: fq.quantize_per_token(x, eye, eye, stream=st),
+                 lambda: fq.quantize_per_token(x, eye, eye, out_dtype="int32", stream=st)):
+        want = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        held = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in (8, 256, 1024, 4096, 16384, 65536)
+                for _ in range(64)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(40_000_000)  # about 20 ms
+        copies = [h.clone() for h in held]
+        del held  # free, and read by the copies that are still queued
+        got = call()
+        torch.cuda.synchronize()
+        assert all(bool((c == 7).all()) for c in copies)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
