@@ -488,8 +488,8 @@ class KVCache:
         qs = self._tokens("q", q, T, None, q.dtype)
         hq, D = q.shape[1], self.head_dim
         batch = self._batch_desc(cu_new, seq_lens, page_table)
-        if max_seq_len is None:
-            max_seq_len = batch.table_width * self.page_size
+        max_q_len = int(max_q_len)  # (of a tensor its value: the sizes below are a key)
+        max_seq_len = batch.table_width * self.page_size if max_seq_len is None else int(max_seq_len)
         if out is None:
             out = _empty(q, (T, hq, D), q.dtype, stream)
         else:
@@ -503,15 +503,15 @@ class KVCache:
         if need is None:
             n = ctypes.c_int64(0)
             _lib.check(self._lib.fq_kv_attention_workspace(self._desc_ref, ctypes.byref(batch), T, hq,
-                                                           int(max_q_len), int(max_seq_len), ctypes.byref(n)),
+                                                           max_q_len, max_seq_len, ctypes.byref(n)),
                        "fq_kv_attention_workspace")
             if len(self._workspace_bytes) >= 4096:
                 self._workspace_bytes.clear()
             need = self._workspace_bytes[sizes] = n.value
         ws = _empty(q, (need,), torch.uint8, stream) if need else None
         st = self._lib.fq_kv_attention(
-            self._desc_ref, ctypes.byref(batch), T, _DT[q.dtype], q.data_ptr(), qs, hq, int(max_q_len),
-            int(max_seq_len), float(scale if scale is not None else D ** -0.5), 1 if causal else 0, out.data_ptr(),
+            self._desc_ref, ctypes.byref(batch), T, _DT[q.dtype], q.data_ptr(), qs, hq, max_q_len,
+            max_seq_len, float(scale if scale is not None else D ** -0.5), 1 if causal else 0, out.data_ptr(),
             lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None, need,
             self._status_ptr, _raw_stream(stream, self._device))
         if st != _lib.FQ_OK:

@@ -387,3 +387,16 @@ def test_memory_of_the_given_stream_in_every_mode():
         torch.cuda.synchronize()
         assert all(bool((c == 7).all()) for c in copies)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_bounds_given_as_tensors_that_change():
+    """max_seq_len as a host tensor that a server counts up in place: the workspace follows its value."""
+    s = Setup([1], [9000], H=1, D=64, page=64, seed=92, width=400).fill()
+    cache, batch = s.cache(), s.batch()
+    q = torch.randn(1, 2, 64, device="cuda").half()
+    longest = torch.tensor(1000)
+    short = (batch[0], torch.tensor([900], dtype=torch.int32, device="cuda"), batch[2])
+    cache.attention(q, *short, max_q_len=1, max_seq_len=longest)
+    longest.fill_(25000)
+    got = cache.attention(q, *batch, max_q_len=1, max_seq_len=longest)
+    assert torch.equal(got, cache.attention(q, *batch, max_q_len=1, max_seq_len=25000)) and cache.device_status() == 0
