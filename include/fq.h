@@ -247,7 +247,8 @@ typedef struct {
  *               formed and reduced in float64, the rotation in float32. rot_dim a multiple of 16,
  *               at most head_dim
  *   q, q_out    [T, q_heads, head_dim] (q tokens q_stride apart, q_out contiguous): the queries,
- *               rotated alike and rounded once to dtype (q_out may be q where q is contiguous);
+ *               rotated alike and rounded once to dtype (q_out may be q where q is contiguous, and
+ *               overlaps no other array);
  *               both NULL with q_heads = 0
  * A page that already holds tokens of the sequence keeps the larger of its exponent and the new
  * tokens'; when it grows, the codes of the older tokens are rounded once more (exact but for
@@ -277,8 +278,9 @@ FQ_API fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch
  *   max_seq_len an upper bound of seq_lens, in [1, table_width * page_size]; a longer sequence is
  *               not computed (FQ_KV_BAD_BATCH). The work is divided by it, so a close bound is
  *               faster
- *   scale       finite
- *   out         [T, q_heads, head_dim] of dtype, contiguous. A query that sees no token gets 0
+ *   scale       finite, at most 1e30 in magnitude
+ *   out         [T, q_heads, head_dim] of dtype, contiguous, apart from q. A query that sees no token
+ *               gets 0
  *   lse         [T, q_heads] float32, or NULL: log sum_j exp(scale * q . key[j]); -inf for a
  *               query that sees no token
  *   workspace   at least fq_kv_attention_workspace(...) bytes, 16-byte aligned (NULL when that is

@@ -97,8 +97,13 @@ __device__ __forceinline__ Quad quad_of(int q, int rot, int interleaved) {
   return z;  // lanes past rot / 4 hold the elements from rot on, four each
 }
 
-template <typename T>
+// kWritten: the kernel may write the row as well (queries in place), so it is not read as constant data.
+template <bool kWritten, typename T>
 __device__ __forceinline__ uint2 load_quad(const T* row, const Quad& z) {
+  if constexpr (kWritten) {
+    if (z.hi == z.lo + 2) return *reinterpret_cast<const uint2*>(row + z.lo);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(row + z.lo), *reinterpret_cast<const uint32_t*>(row + z.hi));
+  }
   if (z.hi == z.lo + 2) return __ldg(reinterpret_cast<const uint2*>(row + z.lo));
   return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row + z.lo)), __ldg(reinterpret_cast<const uint32_t*>(row + z.hi)));
 }
@@ -156,7 +161,7 @@ __device__ __forceinline__ void rotate_queries(const KvAppendParams& p, int64_t 
   for (int k = 0; k < kIter; ++k) {
     const int h = h0 + k * kRps + sub;
     w[k] = make_uint2(0u, 0u);
-    if (h < p.q_heads) w[k] = load_quad(static_cast<const T*>(p.q) + t * p.q_stride + int64_t(h) * D, z);
+    if (h < p.q_heads) w[k] = load_quad<true>(static_cast<const T*>(p.q) + t * p.q_stride + int64_t(h) * D, z);
   }
   const int b = warp_search(p.b.num_seqs, int(t), [&](int i) { return __ldg(p.b.cu_new + i); });
   const int64_t t_first = __ldg(p.b.cu_new + b), t_end = __ldg(p.b.cu_new + b + 1), len = __ldg(p.b.seq_lens + b);
@@ -271,7 +276,7 @@ kv_append_kernel(const KvAppendParams p, const unsigned kv_ctas, const unsigned 
       for (int i = 0; i < kSteps; ++i) {
         const int r = (part + i * wpt) * kRps + sub;
         w[i] = make_uint2(0u, 0u);
-        if (r < rows) w[i] = load_quad(src + r * stride, z);
+        if (r < rows) w[i] = load_quad<false>(src + r * stride, z);
       }
       if (r0 > 0) old = int(*scale) - 127;
 #pragma unroll
