@@ -400,7 +400,8 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         mt_max = fmaxf(mt_max, __shfl_xor_sync(0xffffffffu, mt_max, 4));
         mt_max = fmaxf(mt_max, __shfl_xor_sync(0xffffffffu, mt_max, 8));
         mt_max = fmaxf(mt_max, __shfl_xor_sync(0xffffffffu, mt_max, 16));
-        const float mn = fmaxf(m[n][e], mt_max - kHeadroom);
+        // (rounded up: where scores are so large that 15 is lost beside them, nothing passes 2^15)
+        const float mn = fmaxf(m[n][e], __fsub_ru(mt_max, kHeadroom));
         mu[n][e] = mn == -INFINITY ? 0.0f : mn;  // a row that has seen nothing yet
         alpha[n][e] = fast_exp2(m[n][e] - mu[n][e]);
         m[n][e] = mn;

@@ -33,7 +33,7 @@
 // warps (about 200 clocks each), and a step of one row tile is a chain of softmax (2000 clocks), its
 // hand-over, P V and S (1024), and their hand-over back; the two row tiles' chains overlap, about 3800
 // clocks a step. TMEM: O 2 x D columns, S 2 x 128 columns (P overwrites the first half of its S).
-// Every wait is bounded. A causal prompt of 8192 tokens, 32 heads of 128 on 8: 551 us, 1.0 PFLOP/s.
+// Every wait is bounded. A causal prompt of 8192 tokens, 32 heads of 128 on 8: 569 us, 0.97 PFLOP/s.
 #include <cstdint>
 
 #include "fq_kv_common.cuh"
@@ -64,6 +64,14 @@ constexpr int kNoPage = -1000;  // no exponent
 // Probabilities are taken times 2^kBase for a row's largest score when its reference was set, and the
 // reference is set anew when one passes 2^kMost (fp16 ends at 2^16)
 constexpr float kBase = 12.0f, kMost = 15.9f;
+constexpr int kFarExp = 26;  // see units_of
+// Scores beside which an exponent is lost: from 2^27 on, float32 has steps of 16 and more, which x c - m does
+// not resolve (its product is not rounded). A row whose largest score is as large is computed in units of
+// 2^k, in which it is below 2^27: scores that differ by a step of float32 still differ by 8 then, so that one takes
+// all of the probability, or those that are equal share it.
+__device__ __forceinline__ int units_of(float top) {  // k
+  return max(0, int((__float_as_uint(top) >> 23) & 0xFFu) - 127 - kFarExp);
+}
 
 template <int D>
 struct Geo {
@@ -735,6 +743,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       vis = tr < rows ? int(max(min(v - c0, int64_t(keys)), int64_t(0))) : 0;
     }
     float m = -INFINITY;  // what the row's exponents are taken against (of z log2 e = S * c)
+    int far = 0;          // m and the row's scores are in units of 2^far: see units_of
     int unit = 0;         // of O
     int ahead = 0;        // vis, less what the step's first key is beyond j * kKeys
     float2 l2 = make_float2(0.0f, 0.0f);
@@ -751,7 +760,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         if ((valid & kChange) != 0u) {
           const Step st = bars->step[j & 15];
           ahead = vis - (st.first - j * kKeys);
-          c = fmaxf(c_row * st.k_factor, 1e-37f);  // positive: -inf * c is -inf
+          c = fmaxf(c_row * st.k_factor * exp2i(-far), 1e-37f);  // positive: -inf * c is -inf
           to = st.v_unit;
         }
         valid &= kAllThere;
@@ -779,12 +788,19 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         }
         a0 = max3(a0, x[kKeys - 4], x[kKeys - 3]);
         a1 = max3(a1, x[kKeys - 2], x[kKeys - 1]);
-        const float top = max3(fmaxf(a0, a1), a2, a3) * c;
+        // (rounded up, as the differences to it are: x c - m below takes x c as it is, which then passes neither)
+        float top = __fmul_ru(max3(fmaxf(a0, a1), a2, a3), c);
         // raise the reference where the row is beyond it by 2^kMost (or had none)
-        const bool raise = top > m && !(top - m <= kMost);
+        const bool raise = top > m && !(__fsub_ru(top, m) <= kMost);
         if (__any_sync(0xffffffffu, raise) || to != unit) {
-          float alpha = raise ? (m == -INFINITY ? 0.0f : fast_exp2(m - (top - kBase))) : 1.0f;
-          if (raise) m = top - kBase;
+          float alpha = 1.0f;
+          if (raise) {
+            alpha = m == -INFINITY ? 0.0f : fast_exp2(m - (top - kBase));
+            const int k = units_of(top * exp2i(far));
+            c *= exp2i(far - k);
+            m = __fsub_ru(top * exp2i(far - k), kBase);
+            far = k;
+          }
           l2.x *= alpha;
           l2.y *= alpha;
           alpha *= exp2i(unit - to);
@@ -912,10 +928,10 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           }
         }
         if (live && whole) {
-          if (p.lse != nullptr) p.lse[row] = L != 0.0f ? (m + log2f(L)) * kLn2 : -INFINITY;
+          if (p.lse != nullptr) p.lse[row] = L != 0.0f ? (m + log2f(L)) * exp2i(far) * kLn2 : -INFINITY;
         } else if (live) {
           float* dst = p.ws + (row * p.ws_splits + split) * (D + 4) + D;
-          dst[0] = m;
+          dst[0] = m * exp2i(far);
           dst[1] = L;
         }
       }

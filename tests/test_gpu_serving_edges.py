@@ -400,3 +400,30 @@ def test_bounds_given_as_tensors_that_change():
     longest.fill_(25000)
     got = cache.attention(q, *batch, max_q_len=1, max_seq_len=longest)
     assert torch.equal(got, cache.attention(q, *batch, max_q_len=1, max_seq_len=25000)) and cache.device_status() == 0
+
+
+@pytest.mark.parametrize("new,ctx,G,longest", [([1], [900], 4, None), ([1], [900], 4, 60000), ([3], [200], 2, None),
+                                               ([100], [900], 1, None), ([300], [20], 2, None)])
+@pytest.mark.parametrize("size", [2.0 ** 18, 2.0 ** 24, 2.0 ** 30, 2.0 ** 60])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_far_past_the_exponents_range(new, ctx, G, longest, size, sign):
+    """Scores of 10^5 to 10^20: one key takes all of a row's probability, the output is its value (the
+    values' own half step aside) and lse its score, by the score's float32 roundings."""
+    D = 128
+    s = Setup(new, ctx, H=1, D=D, page=64, seed=93, width=-(-(longest or 1000) // 64)).fill()
+    n = new[0]
+    q = torch.randn(n, G, D, generator=torch.Generator().manual_seed(7)).to(torch.bfloat16)
+    scale = sign * size
+    out, lse = s.cache().attention(q.cuda(), *s.batch(), max_q_len=n, max_seq_len=longest or s.lens[0], scale=scale,
+                                   return_lse=True)
+    k, v = (osv.kv_values(c, x, s.table[0], s.lens[0])[:, 0] for c, x in ((s.k, s.ks), (s.v, s.vs)))
+    z = scale * np.einsum("tgd,jd->tgj", f64(q), k)
+    seen = s.lens[0] - n + np.arange(n) + 1
+    z[np.broadcast_to(np.arange(s.lens[0]) >= seen[:, None, None], z.shape)] = -np.inf
+    at, err = z.argmax(-1), (D * 2.0 ** -23 + 2.0 ** -21) * size * (np.abs(f64(q)) @ np.abs(k).max(0))
+    second = np.sort(z, -1)[..., -2]
+    clear = z.max(-1) - second > 2 * err + 60  # the others are below 2^-86
+    assert clear.mean() > 0.9
+    assert np.all(np.isfinite(f64(out))) and np.all(np.isfinite(f64(lse)))
+    assert np.all(np.abs(f64(out) - v[at])[clear] <= 2.0 ** -8 * np.abs(v[at])[clear])
+    assert np.all(np.abs(f64(lse) - z.max(-1))[clear] <= (err + 2.0 ** -22 * np.abs(z.max(-1)))[clear])
