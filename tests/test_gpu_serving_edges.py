@@ -4,6 +4,7 @@ one stream or thread. Oracles and derived tolerances as in test_gpu_kv.py and te
 unless a test derives its own.
 """
 
+import threading
 import time
 
 import numpy as np
@@ -11,8 +12,9 @@ import pytest
 import torch
 
 from oracle import serving as osv
-from test_gpu_kv import HALF, Setup, f64
-from rotation_bit_quantization_token_b200 import FlatQuant, KVCache, _lib, int8_device_status, int8_matmul, quantize_mx_static
+from test_gpu_kv import HALF, Setup, _check_append, _check_attention, f64
+from rotation_bit_quantization_token_b200 import (FlatQuant, HostPipeline, KVCache, _lib, int8_device_status,
+                                                  int8_matmul, quantize_mx_static)
 
 pytestmark = pytest.mark.gpu
 
@@ -427,3 +429,91 @@ def test_scores_far_past_the_exponents_range(new, ctx, G, longest, size, sign):
     assert np.all(np.isfinite(f64(out))) and np.all(np.isfinite(f64(lse)))
     assert np.all(np.abs(f64(out) - v[at])[clear] <= 2.0 ** -8 * np.abs(v[at])[clear])
     assert np.all(np.abs(f64(lse) - z.max(-1))[clear] <= (err + 2.0 ** -22 * np.abs(z.max(-1)))[clear])
+
+
+def test_two_threads_on_one_cache():
+    """Two threads with a stream each call append and attention on one cache, on pages and sizes of their own."""
+    cache = KVCache(64, 16, 2, 64)
+    sizes = ((1, 300), (40, 200))
+
+    def inputs(i):
+        n, ctx = sizes[i]
+        g = torch.Generator(device="cuda").manual_seed(i)
+        total = n + ctx
+        table = torch.arange(32 * i, 32 * i + 32, dtype=torch.int32, device="cuda")[None]
+        k, v = (torch.randn(total, 2, 64, generator=g, device="cuda").half() for _ in range(2))
+        q = torch.randn(n, 8, 64, generator=g, device="cuda").half()
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        return k, v, q, i32([0, total]), i32([0, n]), i32([total]), table, n, total
+
+    def run(c, k, v, q, cu_all, cu, lens, table, n, total, reps):
+        outs = []
+        for _ in range(reps):
+            c.append(k, v, cu_all, lens, table)
+            outs.append(c.attention(q, cu, lens, table, max_q_len=n, max_seq_len=total))
+        return outs
+
+    data = [inputs(i) for i in range(2)]
+    want = [run(KVCache(64, 16, 2, 64), *d, reps=1)[0] for d in data]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            got[i] = run(cache, *data[i], reps=50)
+        st.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert cache.device_status() == 0
+    for i in range(2):
+        assert len(got[i]) == 50 and all(torch.equal(o, want[i]) for o in got[i])
+
+
+# ------------------------------------------------------------------------------------
+# many sequences, and prompts beside decode steps
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("count", [33, 65, 1100])
+def test_append_many_sequences(count):
+    """More sequences than a warp probes at once, and than two rounds of probes tell apart; some without
+    new tokens."""
+    r = np.random.default_rng(count)
+    new = r.integers(0, 4, count).tolist()
+    s = Setup(new, r.integers(0, 40, count).tolist(), H=1, D=64, page=16, seed=94)
+    _check_append(s, torch.bfloat16, G=2, rot=32, interleaved=False, tail=3)
+
+
+def test_prompts_of_many_sequences():
+    """More sequences than the prompt kernel sorts by length."""
+    r = np.random.default_rng(1)
+    s = Setup([9] * 259 + [1, 0, 20], r.integers(0, 40, 262).tolist(), H=1, D=64, page=16, seed=95).fill()
+    _check_attention(s, torch.bfloat16, G=8)
+
+
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 1)])
+def test_prompts_beside_decode_steps(D, G):
+    """Prompts, whole and in chunks, and decode steps whose contexts are divided into more chunks than a
+    cluster joins, in one call."""
+    s = Setup([200, 1, 1, 130, 3, 0, 1], [0, 9000, 40, 700, 6000, 10, 3000], H=1, D=D, page=64, seed=96).fill()
+    _check_attention(s, torch.bfloat16, G=G, tail=2)
+    _check_attention(s, torch.float16, G=G, causal=False)
+
+
+def test_host_pipeline_int8():
+    """INT8 codes from host memory in slices: those of one call on the device."""
+    K, M, N = 64, 64, 64
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn(K, M, N, generator=g).to(torch.bfloat16)
+    P1, P2 = (torch.linalg.qr(torch.randn(n, n, generator=g))[0].to(torch.bfloat16).contiguous() for n in (M, N))
+    fq = FlatQuant(K, M, N)
+    want = fq.quantize_per_token(x.cuda(), P1.cuda(), P2.cuda(), out_dtype="int8")
+    for chunks in (1, 4):
+        pipe = HostPipeline(fq, "per_token", out_dtype="int8", chunks=chunks)
+        out, scale = pipe.host_outputs()
+        pipe.run(x.pin_memory(), P1.pin_memory(), P2.pin_memory(), out, scale)
+        torch.cuda.synchronize()
+        assert out.dtype is torch.int8 and torch.equal(out, want[0].cpu()) and torch.equal(scale, want[1].cpu())
