@@ -41,10 +41,11 @@ __device__ __forceinline__ float2 unpack16(uint32_t w, int fp16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// Exponent qe such that amax * 2^-qe lies in [2^14, 2^15) (kept where 2^-qe and 2^qe are normal).
+// Exponent qe such that amax * 2^-qe lies in [2^14, 2^15), or below where 2^-qe would not be a number: at
+// most 113, for the largest bfloat16.
 __device__ __forceinline__ int row_exponent(float amax) {
   const int e = int(__float_as_uint(amax) >> 23) - 127 - 14;
-  return min(max(e, -100), 100);
+  return max(e, -126);
 }
 
 // Scale byte of a page as an exponent; a byte that fq_kv_append cannot have written still gives

@@ -517,3 +517,42 @@ def test_host_pipeline_int8():
         pipe.run(x.pin_memory(), P1.pin_memory(), P2.pin_memory(), out, scale)
         torch.cuda.synchronize()
         assert out.dtype is torch.int8 and torch.equal(out, want[0].cpu()) and torch.equal(scale, want[1].cpu())
+
+
+@pytest.mark.parametrize("new,ctx", [([6], [70]), ([100], [70])])
+def test_queries_up_to_the_largest_and_down_to_the_smallest(new, ctx):
+    """Rows of q up to 2^127 and down to 2^-126 with scores scaled back: the same result."""
+    s = Setup(new, ctx, H=1, D=128, page=32, seed=97).fill()
+    base = torch.randint(1, 4, (new[0], 1, 128), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16) * 0.25
+    cache = s.cache()
+    call = lambda e: cache.attention((base * 2.0 ** e).cuda(), *s.batch(), max_q_len=new[0], scale=0.1 * 2.0 ** -e)  # noqa: E731
+    want = call(0)
+    ro, _, info = osv.kv_attention(f64(base), s.k, s.ks, s.v, s.vs, s.cu, s.lens, s.table, 0.1, True)
+    assert np.all(np.abs(f64(want) - ro) <= (2.0 ** -8 + 2.0 ** -10) * info["pv"] + 2.0 ** -17 * info["vmax"][..., None])
+    for e in (98, -98):  # (the scale is at most 1e30)
+        assert torch.equal(call(e), want)
+    # with scores that stay large or small: finite, the largest score's value or the mean
+    for e in (115, 127):
+        out, lse = cache.attention((base * 2.0 ** e).cuda(), *s.batch(), max_q_len=new[0], scale=2.0 ** -99, return_lse=True)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        ro, rl, info = osv.kv_attention(f64(base) * 2.0 ** e, s.k, s.ks, s.v, s.vs, s.cu, s.lens, s.table, 2.0 ** -99, True)
+        err = (128 * 2.0 ** -23 + 2.0 ** -21) * info["a"]
+        assert np.all(np.abs(f64(lse) - rl) <= err + 2.0 ** -13 + 2.0 ** -22 * np.abs(rl))
+
+
+def test_prompt_past_four_gigabytes():
+    """A prompt's pages whose codes lie past 2^32 bytes."""
+    H, D, page, n = 8, 128, 128, 100
+    pages = (1 << 32) // (H * D * page) + 40
+    cache = KVCache(pages, page, H, D)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, total = i32([[pages - 1, 7, pages - 3]]), 2 * page + 9
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn(total, H, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    cache.append(k, v, i32([0, total]), i32([total]), table)
+    q = torch.randn(n, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    out = cache.attention(q, i32([0, n]), i32([total]), table, max_q_len=n)
+    small = KVCache(3, page, H, D)
+    small.append(k, v, i32([0, total]), i32([total]), i32([[0, 1, 2]]))
+    want = small.attention(q, i32([0, n]), i32([total]), i32([[0, 1, 2]]), max_q_len=n)
+    assert cache.device_status() == 0 and torch.equal(out, want)
