@@ -3,8 +3,8 @@
 // Rows are (new token, query head) pairs that share one key / value head (row r of a sequence: token
 // r / G, head r % G of the group, G = q_heads / kv_heads), 8 or 16 of them per CTA, so a decode step
 // reads each cached byte once for the whole group. The kernel is bound by reading the cache: 2 D
-// bytes a token and head: 64 sequences of 500-16000 tokens, 8 heads of 128, take 172 us, 6.0 TB/s; one
-// of 700 tokens takes 7.6 us, which is launch and latency.
+// bytes a token and head: 64 sequences of 500-16000 tokens, 8 heads of 128, take 173 us, 6.0 TB/s (189 us
+// when repeated for long); one of 700 tokens takes 7.6 us, which is launch and latency.
 //
 // One CTA takes its rows and one chunk of keys; its four warps take tiles of 4096 / D keys in turn,
 // each through a ring of its own (TMA boxes of 128-byte rows, swizzled; no barrier between the
