@@ -68,7 +68,7 @@ general_kernel(const GeneralParams p) {
   float* gR = reinterpret_cast<float*>(smem + off);                     // [G]
   off += size_t(G) * sizeof(float);
   float* red = reinterpret_cast<float*>(smem + off);                    // [kThreads/32]
-  __shared__ float s_inv_scale;
+  __shared__ float s_inv_scale, s_up;  // s_up: INT8 codes, see split_reciprocal
 
   const int tid = threadIdx.x;
   const int lane = tid & 31;
@@ -128,6 +128,7 @@ general_kernel(const GeneralParams p) {
           } else {
             // encode; lanes (c, c+1) hold flat elements (f, f+1) because cb and N are even
             float v = per_token ? acc * s_inv_scale : acc * gR[valid ? (f >> 5) : 0];
+            if (p.mode == kModePerToken8) v = acc * s_up * s_inv_scale;
             const float v_hi = __shfl_down_sync(0xffffffffu, v, 1);
             if (p.mode == kModePerToken8) {
               if (valid) p.out[k * MN + f] = uint8_t(int8_byte(v));  // no pairs: any N
@@ -152,6 +153,11 @@ general_kernel(const GeneralParams p) {
           const float qs = per_token_scale(a, p.clip_ratio, p.mode == kModePerToken8 ? 127.0 : 7.0);
           p.quant_scale[k] = qs;
           s_inv_scale = (qs > 0.0f) ? __frcp_rn(qs) : 0.0f;
+          if (p.mode == kModePerToken8) {
+            const float2 r = split_reciprocal(qs);
+            s_up = r.x;
+            s_inv_scale = r.y;
+          }
         }
         __syncthreads();
       } else if (pass == 0 && p.mode == kModeMx) {

@@ -160,6 +160,13 @@ __device__ __forceinline__ uint32_t int8_byte(float v) {
   return uint32_t(q) & 0xFFu;
 }
 
+// 1 / qs as two factors, up and 1 / (qs * up): below 2^-128 the reciprocal is past float32, which INT8
+// codes reach for tokens of 127 times that.
+__device__ __forceinline__ float2 split_reciprocal(float qs) {
+  const float up = qs < 7.888609e-31f /* 2^-100 */ ? 18446744073709551616.0f /* 2^64 */ : 1.0f;
+  return make_float2(up, qs > 0.0f ? __frcp_rn(qs * up) : 0.0f);
+}
+
 // quantScale = fp32(amax / (top / clipRatio)), the division taken in double; top is the
 // largest code (7 for INT4, 127 for INT8).
 __device__ __forceinline__ float per_token_scale(float amax, double clip_ratio, double top = 7.0) {

@@ -958,10 +958,17 @@ tc_kernel(const __grid_constant__ CUtensorMap tmap, const TcParams p) {
           const int q0 = (tok_in_tile * M) >> 5, nq = (M + 31) >> 5;
           for (int qq = 0; qq < nq; ++qq) amax = fmaxf(amax, bars->red[eg][q0 + qq]);
           const float qs = per_token_scale(amax, p.clip_ratio, kMode == kModePerToken8 ? 127.0 : 7.0);
-          const float inv = qs > 0.0f ? __frcp_rn(qs) : 0.0f;
+          float inv = 0.0f, unit = fcrow;
+          if constexpr (kMode == kModePerToken8) {
+            const float2 r = split_reciprocal(qs);
+            unit *= r.x;
+            inv = r.y;
+          } else {
+            inv = qs > 0.0f ? __frcp_rn(qs) : 0.0f;
+          }
           if (row_valid && m_row == 0) p.quant_scale[grow / M] = qs;
 #pragma unroll
-          for (int sg = 0; sg < NS; ++sg) Fseg[sg] = inv * fcrow;
+          for (int sg = 0; sg < NS; ++sg) Fseg[sg] = inv * unit;
         } else {
           named_bar(bar_id, 128);
           // bytes by each rule's common path; a ratio-rule group next to a power of two is

@@ -556,3 +556,29 @@ def test_prompt_past_four_gigabytes():
     small.append(k, v, i32([0, total]), i32([total]), i32([[0, 1, 2]]))
     want = small.attention(q, i32([0, n]), i32([total]), i32([[0, 1, 2]]), max_q_len=n)
     assert cache.device_status() == 0 and torch.equal(out, want)
+
+
+# ------------------------------------------------------------------------------------
+# INT8 codes
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("kernel,K,M,N", [("general", 5, 16, 16), ("general", 4, 7, 33), ("tcgen05", 40, 64, 64),
+                                          ("tcgen05", 20, 128, 112)])
+@pytest.mark.parametrize("exponent", [-112, -122, -125])
+def test_int8_codes_of_tiny_tokens(kernel, K, M, N, exponent):
+    """Tokens of 2^exponent, whose quantScale's reciprocal is past float32 (the scale below 2^-128, the last two). With
+    identity rotations x'' = x and a code is x / quantScale: within half, the scale's own rounding (half a step,
+    2^-150 at the bottom of the range) and the product's two roundings aside."""
+    g = np.random.default_rng([K, M, N])
+    x = torch.from_numpy((g.integers(-128, 129, (K, M * N)) / 128.0).astype(np.float32)).to(torch.bfloat16) * 2.0 ** exponent
+    x[:, 0] = 2.0 ** exponent
+    x[1] = 0.0
+    eye = [torch.eye(n, dtype=torch.bfloat16, device="cuda") for n in (M, N)]
+    codes, qs = FlatQuant(K, M, N, kernel=kernel).quantize_per_token(x.view(K, M, N).cuda(), *eye, out_dtype="int8")
+    s = 2.0 ** exponent / 127
+    want = np.full(K, s)
+    want[1] = 0.0
+    assert np.all(np.abs(f64(qs) - want) <= 2.0 ** -24 * s + 2.0 ** -150)
+    v = f64(x) / s
+    rel = 2.0 ** -22 + 2.0 ** -150 / s
+    off = np.abs(codes.cpu().numpy().astype(np.float64) - v)
+    assert np.all(off <= 0.5 + np.abs(v) * rel), float(off.max())
